@@ -151,6 +151,129 @@ la_status la_decode_step(const void* q, const void* k, const void* v, void* o,
                          float* state, la_dtype dtype, int B, int H, int d_k,
                          int d_v, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated recurrence: the state decays before each token is added,
+ *       S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = q_t^T S_t
+ * with one log gate g_t per token and head (g_t <= 0 decays, 0 keeps, -inf
+ * starts afresh).  g is [B, H, T] ([1, H, T_total] packed, [B, H] for one
+ * token) in `dtype`; NULL means no decay, the recurrence of la_prefill.
+ * Gates below -110 decay by exactly zero.  Positive gates are taken as they
+ * are while the sum of those of any 128 tokens stays below 80.
+ * Inputs are finite apart from gates of -inf: a NaN or infinity in q, k, v or
+ * a gradient may reach every token of the chunk of 128 that holds it.
+ * Outputs may not overlap inputs, other than where a parameter is said to be
+ * updated.  Rows of the packed layout that no sequence covers are neither
+ * read nor written.
+ * ------------------------------------------------------------------------- */
+
+/* Prefill of the gated recurrence, dense or packed; the parameters of
+ * la_prefill, with g.  Two phases: the states at the chunk edges go to the
+ * workspace, then every chunk is computed on its own, so few long sequences
+ * use the whole device too.
+ *   workspace: la_gated_prefill_workspace_size() bytes, 16-byte aligned, free
+ *     for the library until the call's work on `stream` has finished; calls
+ *     that may overlap (and captured graphs that may run at once) need one
+ *     each.  Nothing in it outlives the call.
+ *   max_seqlen: packed mode only, an upper bound on every sequence length
+ *     (0 = unknown); at most 16 runs the few-token kernel, with the
+ *     consequences that la_prefill describes, and needs no workspace.
+ * Kernels: at most 16 tokens per unit and d_v a multiple of 4 that splits a
+ * block (la_gated_prefill_kernel says "short"): one pass over the state.
+ * Otherwise fp32 CUDA cores in chunks of 32 tokens.  Errors:
+ * LA_ERR_INVALID_ARG (as for la_prefill; a workspace that is missing, too
+ * small or misaligned: la_last_cuda_error() then says what was needed),
+ * LA_ERR_UNSUPPORTED (d_k or d_v above 128; T above 2^31 - 1; a state that is
+ * not 16-byte aligned on the few-token path). */
+la_status la_gated_prefill(const void* q, const void* k, const void* v,
+                           const void* g, void* o, float* state,
+                           la_dtype dtype, int B, int H, int64_t T, int d_k,
+                           int d_v, const int32_t* cu_seqlens, int num_seqs,
+                           int64_t max_seqlen, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace la_gated_prefill needs for these arguments. */
+size_t la_gated_prefill_workspace_size(la_dtype dtype, int B, int H, int64_t T,
+                                       int d_k, int d_v, int num_seqs);
+
+/* Which kernel la_gated_prefill runs: max_tokens is T for dense input and
+ * max_seqlen for packed input.  "short", "simt" or "unsupported".  Host
+ * only. */
+const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens,
+                                    int d_k, int d_v);
+
+/* Gradient of la_gated_prefill (with g == NULL: of la_prefill).
+ *   q, k, v, g, state0: the prefill's inputs; state0 is S_0 (NULL: zero), the
+ *     state as it was before the prefill.
+ *   d_o: gradient of o.
+ *   dstate: [units][d_k][d_v] float32, updated in place: the gradient of S_T
+ *     on entry, of S_0 on return (an empty sequence leaves it as it is).
+ *   dq, dk, dv, dg: gradients of q, k, v and g, written, in `dtype`; dg may be
+ *     NULL.  The gradient of a gate that decays to zero is zero.
+ *   workspace: la_gated_prefill_backward_workspace_size() bytes, as above.
+ * Nothing is taken from the forward call but its inputs: the states are made
+ * again.  Results do not depend on any order of execution.  Errors as for
+ * la_gated_prefill. */
+la_status la_gated_prefill_backward(const void* q, const void* k,
+                                    const void* v, const void* g,
+                                    const float* state0, const void* d_o,
+                                    float* dstate, void* dq, void* dk,
+                                    void* dv, void* dg, la_dtype dtype, int B,
+                                    int H, int64_t T, int d_k, int d_v,
+                                    const int32_t* cu_seqlens, int num_seqs,
+                                    void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+size_t la_gated_prefill_backward_workspace_size(la_dtype dtype, int B, int H,
+                                                int64_t T, int d_k, int d_v,
+                                                int num_seqs);
+
+/* One token of the gated recurrence for every unit: S' = e^g S + k v^T,
+ * o = q^T S'.  As la_decode_step, with g: [B, H]. */
+la_status la_gated_decode_step(const void* q, const void* k, const void* v,
+                               const void* g, void* o, float* state,
+                               la_dtype dtype, int B, int H, int d_k, int d_v,
+                               void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions of q and k, before they enter the recurrence.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    LA_ROTARY_PLAIN = 0,  /* freq[i] = base^(-2i / rot) */
+    LA_ROTARY_LINEAR = 1, /* divided by factor (positions interpolated) */
+    LA_ROTARY_NTK = 2,    /* base * factor^(rot / (rot - 2)): slow pairs stretched, fast ones kept */
+    LA_ROTARY_PARTS = 3   /* by parts: a pair that turns beta_fast times or more within `original`
+                           * positions keeps its frequency, one that turns beta_slow times or fewer
+                           * has it divided by factor, linear in the turns between */
+} la_rotary_scaling;
+
+/* Frequencies of the pairs, freq[rot / 2] float32 on the device, written.
+ * Computed in float64.  Errors: LA_ERR_INVALID_ARG (rot odd or negative, base
+ * or a used parameter not positive, beta_fast <= beta_slow). */
+la_status la_rotary_init(float* freq, int rot, double base,
+                         la_rotary_scaling scaling, double factor,
+                         double original, double beta_fast, double beta_slow,
+                         void* stream);
+
+/* Turns pair i of every head by position * freq[i] and multiplies it by
+ * `scale` (the attention factor of a stretched table, else 1):
+ *   q, k: [B, H, T, d] in `dtype`; k and k_out may both be NULL.
+ *   q_out, k_out: written; each may be its input (in place), no other overlap.
+ *   rot: elements 0 .. rot-1 of a head turn (even, at most d), the others are
+ *     passed through.  Pair i is elements i and i + rot/2, or with
+ *     `interleaved` elements 2i and 2i + 1.
+ *   start: device int32, the position of the first token of every batch entry
+ *     ([B]) or packed sequence ([num_seqs]); NULL: 0.
+ *   inverse: turn back.  The gradient of la_rotary is la_rotary of the
+ *     gradient with `inverse` and the same scale.
+ * Angles are taken in float64, so far positions lose nothing.  Packed rows
+ * before the first and behind the last sequence are left as they are.
+ * Errors: LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED (d above 128). */
+la_status la_rotary(const void* q, const void* k, void* q_out, void* k_out,
+                    la_dtype dtype, int B, int H, int64_t T, int d, int rot,
+                    const float* freq, const int32_t* start, float scale,
+                    int interleaved, int inverse, const int32_t* cu_seqlens,
+                    int num_seqs, void* stream);
+
 /* Synchronises `stream`, then reports and clears the device error word of
  * the current device: LA_ERR_TIMEOUT if a kernel gave up a bounded wait
  * (its outputs are then undefined), LA_ERR_INVALID_ARG if a packed sequence
@@ -186,7 +309,8 @@ const char* la_prefill_kernel(la_dtype dtype, int64_t max_tokens, int d_k,
 int la_resolve_chunk(la_dtype dtype, int d_k, int d_v, int chunk);
 
 /* Text of a status code, and of the last CUDA error seen by this library
- * on the calling thread ("" if none). */
+ * on the calling thread ("" if none).  A refusal by an entry point of the
+ * gated recurrence or of the rotary positions leaves its reason there. */
 const char* la_status_string(la_status s);
 const char* la_last_cuda_error(void);
 

@@ -16,4 +16,6 @@ from .binding import (  # noqa: F401
     la_state_init, la_prefill, la_prefill_workspace_size, la_decode_step,
     la_device_status, la_status_string, la_prefill_path, la_prefill_kernel, la_resolve_chunk,
     la_selftest_wait_timeout,
+    la_gated_prefill, la_gated_prefill_workspace_size, la_gated_prefill_kernel, la_gated_decode_step,
+    la_gated_prefill_backward, la_gated_prefill_backward_workspace_size, la_rotary, la_rotary_init,
 )

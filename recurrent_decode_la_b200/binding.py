@@ -29,7 +29,7 @@ _lock = threading.Lock()
 class LinAttnError(RuntimeError):
     def __init__(self, status: int, where: str):
         msg = f"{where}: {la_status_string(status)}"
-        if status == LA_ERR_CUDA:
+        if status == LA_ERR_CUDA or where.startswith(("la_gated", "la_rotary")):  # these say why they refuse
             msg += f" ({last_cuda_error()})"
         super().__init__(msg)
         self.status = status
@@ -68,6 +68,20 @@ def load_library():
         lib.la_status_string.argtypes = [i32]
         lib.la_status_string.restype = ctypes.c_char_p
         lib.la_last_cuda_error.restype = ctypes.c_char_p
+        lib.la_gated_prefill.argtypes = [vp] * 6 + [i32, i32, i32, i64, i32, i32, vp, i32, i64, vp, sz, vp]
+        lib.la_gated_prefill_backward.argtypes = [vp] * 11 + [i32, i32, i32, i64, i32, i32, vp, i32, vp, sz, vp]
+        lib.la_gated_decode_step.argtypes = [vp] * 6 + [i32, i32, i32, i32, i32, vp]
+        for name in ("la_gated_prefill_workspace_size", "la_gated_prefill_backward_workspace_size"):
+            getattr(lib, name).argtypes = [i32, i32, i32, i64, i32, i32, i32]
+            getattr(lib, name).restype = sz
+        lib.la_gated_prefill_kernel.argtypes = [i32, i64, i32, i32]
+        lib.la_gated_prefill_kernel.restype = ctypes.c_char_p
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        lib.la_rotary_init.argtypes = [vp, i32, f64, i32, f64, f64, f64, f64, vp]
+        lib.la_rotary.argtypes = [vp, vp, vp, vp, i32, i32, i32, i64, i32, i32, vp, vp, f32, i32, i32, vp, i32, vp]
+        for name in ("la_gated_prefill", "la_gated_prefill_backward", "la_gated_decode_step", "la_rotary_init",
+                     "la_rotary"):
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("la_state_init", "la_prefill", "la_decode_step", "la_device_status",
                      "la_resolve_chunk"):
             getattr(lib, name).restype = ctypes.c_int
@@ -218,3 +232,190 @@ def la_prefill_kernel(dtype: torch.dtype, max_tokens: int, dk: int, dv: int, chu
 
 def la_resolve_chunk(dtype: torch.dtype, dk: int, dv: int, chunk: int = 0) -> int:
     return int(load_library().la_resolve_chunk(_DTYPES[dtype], dk, dv, chunk))
+
+
+# ---------------------------------------------------------------------------
+# The gated recurrence and rotary positions
+# ---------------------------------------------------------------------------
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+def _call(name: str, device: torch.device, stream, *args) -> None:
+    """Run one entry point with the tensors' device current, on its current
+    stream unless one is given."""
+    lib = load_library()
+    with torch.cuda.device(device):
+        _check(getattr(lib, name)(*args, _stream(torch.cuda.current_stream(device) if stream is None else stream)),
+               name)
+
+
+def _one_device(**tensors: Optional[torch.Tensor]) -> torch.device:
+    devs = {n: t.device for n, t in tensors.items() if t is not None}
+    first = next(iter(devs.values()))
+    for n, d in devs.items():
+        if d != first:
+            raise ValueError(f"{n} is on {d}, not on {first}")
+    return first
+
+
+def _expect(t: torch.Tensor, shape, name: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _sequences(q, k, v, cu_seqlens, state, name: str):
+    """Shape checks that the sequence entry points share: (B, H, T, dk, dv, num_seqs)."""
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B, H, T, d_k] and v [B, H, T, d_v]")
+    B, H, T, dk = q.shape
+    dv = v.shape[-1]
+    _expect(k, q.shape, "k")
+    _expect(v, (B, H, T, dv), "v")
+    num_seqs = _packed(cu_seqlens, B)
+    n_units = (num_seqs if cu_seqlens is not None else B) * H
+    if state.numel() != n_units * dk * dv:
+        raise ValueError(f"{name} must hold {n_units} x {dk} x {dv} floats "
+                         f"({'num_seqs' if cu_seqlens is not None else 'B'} * H units), got {state.numel()}")
+    return B, H, T, dk, dv, num_seqs
+
+
+def _packed(cu_seqlens: Optional[torch.Tensor], B: int) -> int:
+    if cu_seqlens is None:
+        return 0
+    if cu_seqlens.dtype != torch.int32:
+        raise ValueError("cu_seqlens must be int32")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+    if B != 1:
+        raise ValueError("packed input (cu_seqlens) needs B == 1")
+    return cu_seqlens.numel() - 1
+
+
+def _workspace(workspace: Optional[torch.Tensor]):
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def la_gated_prefill_workspace_size(dtype: torch.dtype, B: int, H: int, T: int, dk: int, dv: int,
+                                    num_seqs: int = 0) -> int:
+    return int(load_library().la_gated_prefill_workspace_size(_DTYPES[dtype], B, H, T, dk, dv, num_seqs))
+
+
+def la_gated_prefill_backward_workspace_size(dtype: torch.dtype, B: int, H: int, T: int, dk: int, dv: int,
+                                             num_seqs: int = 0) -> int:
+    return int(load_library().la_gated_prefill_backward_workspace_size(_DTYPES[dtype], B, H, T, dk, dv, num_seqs))
+
+
+def la_gated_prefill_kernel(dtype: torch.dtype, max_tokens: int, dk: int, dv: int) -> str:
+    """Which kernel la_gated_prefill runs ("short", "tc", "simt" or "unsupported").
+    max_tokens: T (dense) or max_seqlen (packed)."""
+    return load_library().la_gated_prefill_kernel(_DTYPES[dtype], int(max_tokens), dk, dv).decode()
+
+
+def la_gated_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor],
+                     o: torch.Tensor, state: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                     max_seqlen: int = 0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Prefill of S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = q_t^T S_t.  q, k [B,H,T,d_k]; v, o [B,H,T,d_v];
+    g [B,H,T] log gates (None: no decay); state as for la_prefill."""
+    B, H, T, dk, dv, num_seqs = _sequences(q, k, v, cu_seqlens, state, "state")
+    _expect(o, v.shape, "o")
+    if g is not None:
+        _expect(g, (B, H, T), "g")
+    dt = q.dtype
+    dev = _one_device(q=q, k=k, v=v, g=g, o=o, state=state, cu_seqlens=cu_seqlens, workspace=workspace)
+    ws, ws_bytes = _workspace(workspace)
+    _call("la_gated_prefill", dev, stream, _ptr(q, "q", dt), _ptr(k, "k", dt), _ptr(v, "v", dt), _ptr(g, "g", dt),
+          _ptr(o, "o", dt), _ptr(state, "state", torch.float32), _DTYPES[dt], B, H, T, dk, dv,
+          _ptr(cu_seqlens, "cu_seqlens"), num_seqs, int(max_seqlen), ws, ws_bytes)
+
+
+def la_gated_prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor],
+                              state0: Optional[torch.Tensor], do: torch.Tensor, dstate: torch.Tensor,
+                              dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, dg: Optional[torch.Tensor] = None,
+                              cu_seqlens: Optional[torch.Tensor] = None, max_seqlen: int = 0,
+                              workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradient of la_gated_prefill.  state0: the incoming state (None: zero); dstate: gradient of the final state
+    on entry, of the incoming one on return; dq, dk, dv, dg are written.  max_seqlen is not needed and taken only so
+    that both directions can be called alike."""
+    B, H, T, d_k, d_v, num_seqs = _sequences(q, k, v, cu_seqlens, dstate, "dstate")
+    for name, t, like in (("do", do, v), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _expect(t, like.shape, name)
+    for name, t in (("g", g), ("dg", dg)):
+        if t is not None:
+            _expect(t, (B, H, T), name)
+    if state0 is not None and state0.numel() != dstate.numel():
+        raise ValueError("state0 must hold as many floats as dstate")
+    dt = q.dtype
+    dev = _one_device(q=q, k=k, v=v, g=g, state0=state0, do=do, dstate=dstate, dq=dq, dk=dk, dv=dv, dg=dg,
+                      cu_seqlens=cu_seqlens, workspace=workspace)
+    ws, ws_bytes = _workspace(workspace)
+    _call("la_gated_prefill_backward", dev, stream, _ptr(q, "q", dt), _ptr(k, "k", dt), _ptr(v, "v", dt),
+          _ptr(g, "g", dt), _ptr(state0, "state0", torch.float32), _ptr(do, "do", dt),
+          _ptr(dstate, "dstate", torch.float32), _ptr(dq, "dq", dt), _ptr(dk, "dk", dt), _ptr(dv, "dv", dt),
+          _ptr(dg, "dg", dt), _DTYPES[dt], B, H, T, d_k, d_v, _ptr(cu_seqlens, "cu_seqlens"), num_seqs, ws, ws_bytes)
+
+
+def la_gated_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor],
+                         o: torch.Tensor, state: torch.Tensor, stream=None) -> None:
+    """One token per unit: S <- e^g S + k v^T, o = q^T S.  q, k [B,H,d_k]; v, o [B,H,d_v]; g [B,H]."""
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [B, H, d_k] and v [B, H, d_v]")
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    _expect(k, q.shape, "k")
+    _expect(v, (B, H, dv), "v")
+    _expect(o, v.shape, "o")
+    if g is not None:
+        _expect(g, (B, H), "g")
+    if state.numel() != B * H * dk * dv:
+        raise ValueError(f"state must hold {B * H} x {dk} x {dv} floats, got {state.numel()}")
+    dt = q.dtype
+    dev = _one_device(q=q, k=k, v=v, g=g, o=o, state=state)
+    _call("la_gated_decode_step", dev, stream, _ptr(q, "q", dt), _ptr(k, "k", dt), _ptr(v, "v", dt),
+          _ptr(g, "g", dt), _ptr(o, "o", dt), _ptr(state, "state", torch.float32), _DTYPES[dt], B, H, dk, dv)
+
+
+def la_rotary_init(freq: torch.Tensor, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                   original: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, stream=None) -> None:
+    """freq [rot / 2] float32 <- the pairs' frequencies.  scaling: "plain", "linear", "ntk" or "parts"."""
+    if freq.dim() != 1:
+        raise ValueError("freq must be [rot / 2]")
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}, got {scaling!r}")
+    _call("la_rotary_init", freq.device, stream, _ptr(freq, "freq", torch.float32), 2 * freq.numel(), float(base),
+          ROTARY_SCALINGS[scaling], float(factor), float(original), float(beta_fast), float(beta_slow))
+
+
+def la_rotary(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor, k_out: Optional[torch.Tensor],
+              freq: torch.Tensor, start: Optional[torch.Tensor] = None, scale: float = 1.0,
+              interleaved: bool = False, inverse: bool = False, cu_seqlens: Optional[torch.Tensor] = None,
+              stream=None) -> None:
+    """Turn the first 2 * len(freq) elements of every head by their positions.  q, k [B,H,T,d]; freq [rot / 2];
+    start int32 [B] (or [num_seqs] with cu_seqlens): the first token's position.  The outputs may be the inputs."""
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, T, d]")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    B, H, T, d = q.shape
+    for name, t in (("k", k), ("q_out", q_out), ("k_out", k_out)):
+        if t is not None:
+            _expect(t, q.shape, name)
+    if freq.dim() != 1 or 2 * freq.numel() > d:
+        raise ValueError("freq must be [rot / 2] with rot <= d")
+    num_seqs = _packed(cu_seqlens, B)
+    if start is not None:
+        if start.dtype != torch.int32:
+            raise ValueError("start must be int32")
+        _expect(start, (num_seqs if cu_seqlens is not None else B,), "start")
+    dt = q.dtype
+    dev = _one_device(q=q, k=k, q_out=q_out, k_out=k_out, freq=freq, start=start, cu_seqlens=cu_seqlens)
+    _call("la_rotary", dev, stream, _ptr(q, "q", dt), _ptr(k, "k", dt), _ptr(q_out, "q_out", dt),
+          _ptr(k_out, "k_out", dt), _DTYPES[dt], B, H, T, d, 2 * freq.numel(), _ptr(freq, "freq", torch.float32),
+          _ptr(start, "start"), float(scale), int(interleaved), int(inverse), _ptr(cu_seqlens, "cu_seqlens"), num_seqs)

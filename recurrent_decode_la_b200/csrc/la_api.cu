@@ -51,15 +51,17 @@ const Tuning& tuning() {
     return t;
 }
 
-namespace {
+static thread_local char g_last_cuda_error[256] = "";
 
-thread_local char g_last_cuda_error[256] = "";
+void set_last_error(const char* text) { snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s", text); }
 
-la_status cuda_fail(cudaError_t e) {
+int cuda_fail_status(cudaError_t e) {
     snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s", cudaGetErrorName(e),
              cudaGetErrorString(e));
     return LA_ERR_CUDA;
 }
+
+static la_status cuda_fail(cudaError_t e) { return static_cast<la_status>(cuda_fail_status(e)); }
 
 int current_sm_count() {
     static std::atomic<int> cache[64];  // static storage: zero-initialised
@@ -74,6 +76,8 @@ int current_sm_count() {
     if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
     return n;
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -105,8 +109,8 @@ CUcontext current_context() {
     return c;
 }
 
-// 3-D bf16 view (d, rows, groups) of a [groups][rows][d] tensor, box
-// (64, chunk, 1), 128-byte swizzle: one box fills one swizzled smem panel.
+}  // namespace
+
 bool encode_bf16_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_t groups, int chunk) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
@@ -120,6 +124,8 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, int d, int64_t rows, in
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 int default_chunk(la_dtype dtype, int dk, int dv) {
     if (tuning().chunk > 0) return tuning().chunk;
@@ -302,7 +308,7 @@ la_status la_prefill(const void* q, const void* k, const void* v, void* o, float
     if (path == kUnsupported) return LA_ERR_UNSUPPORTED;
 
     PrefillProblem p;
-    p.q = q; p.k = k; p.v = v; p.o = o; p.state = state;
+    p.q = q; p.k = k; p.v = v; p.g = nullptr; p.o = o; p.state = state;
     p.dtype = dtype == LA_BF16 ? 1 : 0;
     p.H = H > 0 ? H : 1;
     p.rows_per_group = T;
@@ -390,7 +396,7 @@ la_status la_decode_step(const void* q, const void* k, const void* v, void* o, f
     const int64_t n_units = static_cast<int64_t>(B) * H;
     if (n_units == 0) return LA_OK;
     if (!q || !k || !v || !o || !state) return LA_ERR_INVALID_ARG;
-    cudaError_t e = launch_decode(q, k, v, o, state, dtype == LA_BF16 ? 1 : 0, n_units, d_k, d_v,
+    cudaError_t e = launch_decode(q, k, v, nullptr, o, state, dtype == LA_BF16 ? 1 : 0, n_units, d_k, d_v,
                                   current_sm_count(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LA_OK : cuda_fail(e);
 }

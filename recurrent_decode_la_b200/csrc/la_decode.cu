@@ -12,6 +12,10 @@
 // and v entries it needs itself, updates the rows, stores them back, and
 // keeps a partial q^T S' for its columns; the partials of the rows are
 // summed by warp shuffles, then across warps in shared memory.
+//
+// The gated step is S' = a S + k v^T with a = e^g, one log gate a unit: the
+// same kernels with one multiplication more per state element (GATED), which
+// the memory traffic hides.
 #include <cuda_bf16.h>
 
 #include "la_internal.h"
@@ -60,6 +64,21 @@ __device__ __forceinline__ float4 dec_in4<__nv_bfloat16>(const __nv_bfloat16* p)
     return make_float4(__bfloat162float(p[0]), __bfloat162float(p[1]), __bfloat162float(p[2]), __bfloat162float(p[3]));
 }
 
+// The decay e^g of a unit (1 without gates), and its application.
+template <bool GATED, typename T>
+__device__ __forceinline__ float dec_gate(const T* g, int64_t u) {
+    return GATED ? expf(dec_in<T>(g, u)) : 1.f;
+}
+template <bool GATED>
+__device__ __forceinline__ void dec_scale(float4& s, float a) {
+    if constexpr (GATED) {
+        s.x *= a;
+        s.y *= a;
+        s.z *= a;
+        s.w *= a;
+    }
+}
+
 // Bring the 128-byte line holding p into L2 (a hint: no data is returned).
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
@@ -69,11 +88,11 @@ constexpr int kDecThreads = 256;
 constexpr int kDecMaxRowsPerThread = 16;
 
 // Vector form: d_v / 4 divides 256, state rows 16-byte aligned.
-template <typename T>
+template <typename T, bool GATED>
 __global__ void __launch_bounds__(kDecThreads) decode_vec_kernel(const T* __restrict__ q, const T* __restrict__ k,
-                                                                 const T* __restrict__ v, T* __restrict__ o,
-                                                                 float* __restrict__ state, int64_t n_units,
-                                                                 int dk, int dv) {
+                                                                 const T* __restrict__ v, const T* __restrict__ g,
+                                                                 T* __restrict__ o, float* __restrict__ state,
+                                                                 int64_t n_units, int dk, int dv) {
     extern __shared__ float sm[];
     float* qs = sm;
     float* ks = qs + 128;
@@ -97,6 +116,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_vec_kernel(const T* __rest
             const int r = r0 + i * rpp;
             if (r < dk) sv[i] = S[r * cols4 + c4];
         }
+        const float a = dec_gate<GATED>(g, u);
         __syncthreads();
         const float4 vv = make_float4(vs[4 * c4], vs[4 * c4 + 1], vs[4 * c4 + 2], vs[4 * c4 + 3]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -106,6 +126,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_vec_kernel(const T* __rest
             if (r < dk) {
                 const float kr = ks[r], qr = qs[r];
                 float4 s = sv[i];
+                dec_scale<GATED>(s, a);
                 s.x = fmaf(kr, vv.x, s.x);
                 s.y = fmaf(kr, vv.y, s.y);
                 s.z = fmaf(kr, vv.z, s.z);
@@ -152,10 +173,11 @@ __global__ void __launch_bounds__(kDecThreads) decode_vec_kernel(const T* __rest
 // rows per thread with every index known to the compiler.  NT threads per
 // CTA: 256 (four CTAs per SM), or 1024 for few units (fewer, larger CTAs
 // launch faster; each thread then holds two rows).
-template <typename T, int NR, int FDK, int FNC, int NT = kDecThreads>
+template <typename T, bool GATED, int NR, int FDK, int FNC, int NT = kDecThreads>
 __global__ void __launch_bounds__(NT, (NT >= 1024 ? 1 : 4))
-    decode_cols_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, T* __restrict__ o,
-                       float* __restrict__ state, int64_t n_units, int dk_arg, int dv_arg, int cb_count) {
+    decode_cols_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                       const T* __restrict__ g, T* __restrict__ o, float* __restrict__ state, int64_t n_units,
+                       int dk_arg, int dv_arg, int cb_count) {
     extern __shared__ float sm[];
     float* red = sm;  // [warps][cols of this CTA]
     const int dk = FDK > 0 ? FDK : dk_arg;
@@ -196,6 +218,7 @@ __global__ void __launch_bounds__(NT, (NT >= 1024 ? 1 : 4))
     // of its own columns itself (the CTA's threads share them through L1), so
     // no block barrier stands between the loads and the arithmetic
     const T* vc = v + u * dv + cbeg + 4 * c4;
+    const float a = dec_gate<GATED>(g, u);
     const float4 vv = dec_in4<T>(vc);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if constexpr (FDK > 0) {
@@ -211,6 +234,7 @@ __global__ void __launch_bounds__(NT, (NT >= 1024 ? 1 : 4))
         for (int i = 0; i < NR; ++i) {
             const int r = r0 + i * rpp;
             float4 s4 = sv[i];
+            dec_scale<GATED>(s4, a);
             s4.x = fmaf(kr[i], vv.x, s4.x);
             s4.y = fmaf(kr[i], vv.y, s4.y);
             s4.z = fmaf(kr[i], vv.z, s4.z);
@@ -237,6 +261,7 @@ __global__ void __launch_bounds__(NT, (NT >= 1024 ? 1 : 4))
             if (r < dk) {
                 const float kr = dec_in<T>(ku, r), qr = dec_in<T>(qu, r);
                 float4 s4 = sv[i];
+                dec_scale<GATED>(s4, a);
                 s4.x = fmaf(kr, vv.x, s4.x);
                 s4.y = fmaf(kr, vv.y, s4.y);
                 s4.z = fmaf(kr, vv.z, s4.z);
@@ -269,11 +294,11 @@ __global__ void __launch_bounds__(NT, (NT >= 1024 ? 1 : 4))
 }
 
 // Scalar form for any d_k, d_v <= 128 and any alignment.
-template <typename T>
+template <typename T, bool GATED>
 __global__ void __launch_bounds__(kDecThreads) decode_scalar_kernel(const T* __restrict__ q, const T* __restrict__ k,
-                                                                    const T* __restrict__ v, T* __restrict__ o,
-                                                                    float* __restrict__ state, int64_t n_units,
-                                                                    int dk, int dv) {
+                                                                    const T* __restrict__ v, const T* __restrict__ g,
+                                                                    T* __restrict__ o, float* __restrict__ state,
+                                                                    int64_t n_units, int dk, int dv) {
     extern __shared__ float sm[];
     float* qs = sm;
     float* ks = qs + 128;
@@ -291,10 +316,11 @@ __global__ void __launch_bounds__(kDecThreads) decode_scalar_kernel(const T* __r
         for (int i = tid; i < dv; i += kDecThreads) vs[i] = dec_in<T>(v, u * dv + i);
         __syncthreads();
         float* S = state + u * static_cast<int64_t>(dk) * dv;
+        const float a = dec_gate<GATED>(g, u);
         float acc = 0.f;
         if (r0 < rpp) {
             for (int r = r0; r < dk; r += rpp) {
-                const float s = fmaf(ks[r], vs[c], S[r * dv + c]);
+                const float s = fmaf(ks[r], vs[c], GATED ? a * S[r * dv + c] : S[r * dv + c]);
                 S[r * dv + c] = s;
                 acc = fmaf(qs[r], s, acc);
             }
@@ -310,8 +336,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_scalar_kernel(const T* __r
     }
 }
 
-template <typename T>
-static cudaError_t launch_cols(const T* q, const T* k, const T* v, T* o, float* state, int64_t n_units, int dk,
+template <typename T, bool GATED>
+static cudaError_t launch_cols(const T* q, const T* k, const T* v, const T* g, T* o, float* state, int64_t n_units, int dk,
                                int dv, int cb, bool big, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n_units * cb), 1, 1);
@@ -326,27 +352,27 @@ static cudaError_t launch_cols(const T* q, const T* k, const T* v, T* o, float* 
     const int ncol = dv / cb;
     const bool sq = (dk == dv);
     if (big && dk == 128)  // two 1024-thread CTAs per unit, 64 columns each
-        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 2, 128, 64, 1024>, q, k, v, o, state, n_units, dk, dv,
+        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 2, 128, 64, 1024>, q, k, v, g, o, state, n_units, dk, dv,
                                   cb);
     if (big)  // d = 64: one 1024-thread CTA per unit
-        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 1, 64, 64, 1024>, q, k, v, o, state, n_units, dk, dv,
+        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 1, 64, 64, 1024>, q, k, v, g, o, state, n_units, dk, dv,
                                   cb);
     if (sq && dk == 128 && ncol == 32)
-        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 4, 128, 32>, q, k, v, o, state, n_units, dk, dv, cb);
+        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 4, 128, 32>, q, k, v, g, o, state, n_units, dk, dv, cb);
     if (sq && dk == 128 && ncol == 16)
-        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 2, 128, 16>, q, k, v, o, state, n_units, dk, dv, cb);
+        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 2, 128, 16>, q, k, v, g, o, state, n_units, dk, dv, cb);
     if (sq && dk == 64 && ncol == 32)
-        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 2, 64, 32>, q, k, v, o, state, n_units, dk, dv, cb);
+        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 2, 64, 32>, q, k, v, g, o, state, n_units, dk, dv, cb);
     if (sq && dk == 64 && ncol == 16)
-        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 1, 64, 16>, q, k, v, o, state, n_units, dk, dv, cb);
+        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 1, 64, 16>, q, k, v, g, o, state, n_units, dk, dv, cb);
     // other shapes: rows per thread held in registers at once, batches of up to 4
     const int rpp = kDecThreads / (ncol / 4);
     const int need = (dk + rpp - 1) / rpp;
     if (need <= 1)
-        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 1, 0, 0>, q, k, v, o, state, n_units, dk, dv, cb);
+        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 1, 0, 0>, q, k, v, g, o, state, n_units, dk, dv, cb);
     if (need <= 2)
-        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 2, 0, 0>, q, k, v, o, state, n_units, dk, dv, cb);
-    return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, 4, 0, 0>, q, k, v, o, state, n_units, dk, dv, cb);
+        return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 2, 0, 0>, q, k, v, g, o, state, n_units, dk, dv, cb);
+    return cudaLaunchKernelEx(&cfg, decode_cols_kernel<T, GATED, 4, 0, 0>, q, k, v, g, o, state, n_units, dk, dv, cb);
 }
 
 // Column blocks per unit for the 256-thread form: 32 columns per CTA where
@@ -365,9 +391,10 @@ static int decode_col_blocks(int64_t n_units, int num_sms, int dk, int dv) {
     return ok(cb) ? cb : 0;
 }
 
-cudaError_t launch_decode(const void* q, const void* k, const void* v, void* o, float* state,
-                          int dtype, int64_t n_units, int dk, int dv, int num_sms, cudaStream_t s) {
-    if (n_units <= 0) return cudaSuccess;
+// The whole choice for one element type.
+template <typename T, bool GATED>
+static cudaError_t launch_decode_t(const T* q, const T* k, const T* v, const T* g, T* o, float* state,
+                                   int64_t n_units, int dk, int dv, int num_sms, cudaStream_t s) {
     const unsigned grid = static_cast<unsigned>(n_units < 2147483647 ? n_units : 2147483647);
     const size_t smem = sizeof(float) * (3 * 128 + 1024);
     const int cols4 = dv / 4;
@@ -392,37 +419,29 @@ cudaError_t launch_decode(const void* q, const void* k, const void* v, void* o, 
     }
     if (cb > 0 && (dv % (4 * cb) != 0 || kDecThreads % (dv / (4 * cb)) != 0)) cb = 0;
     if (cb > 0) {
-        cudaError_t e;
-        if (dtype == 0)
-            e = launch_cols<float>(static_cast<const float*>(q), static_cast<const float*>(k),
-                                   static_cast<const float*>(v), static_cast<float*>(o), state, n_units, dk, dv, cb,
-                                   big, s);
-        else
-            e = launch_cols<__nv_bfloat16>(static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-                                           static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o), state,
-                                           n_units, dk, dv, cb, big, s);
+        const cudaError_t e = launch_cols<T, GATED>(q, k, v, g, o, state, n_units, dk, dv, cb, big, s);
         if (e != cudaSuccess) return e;
         return cudaGetLastError();
     }
-    if (dtype == 0) {
-        const float *qq = static_cast<const float*>(q), *kk = static_cast<const float*>(k),
-                    *vv = static_cast<const float*>(v);
-        float* oo = static_cast<float*>(o);
-        if (vec)
-            decode_vec_kernel<float><<<grid, kDecThreads, smem, s>>>(qq, kk, vv, oo, state, n_units, dk, dv);
-        else
-            decode_scalar_kernel<float><<<grid, kDecThreads, smem, s>>>(qq, kk, vv, oo, state, n_units, dk, dv);
-    } else {
-        const __nv_bfloat16 *qq = static_cast<const __nv_bfloat16*>(q),
-                            *kk = static_cast<const __nv_bfloat16*>(k),
-                            *vv = static_cast<const __nv_bfloat16*>(v);
-        __nv_bfloat16* oo = static_cast<__nv_bfloat16*>(o);
-        if (vec)
-            decode_vec_kernel<__nv_bfloat16><<<grid, kDecThreads, smem, s>>>(qq, kk, vv, oo, state, n_units, dk, dv);
-        else
-            decode_scalar_kernel<__nv_bfloat16><<<grid, kDecThreads, smem, s>>>(qq, kk, vv, oo, state, n_units, dk, dv);
-    }
+    if (vec)
+        decode_vec_kernel<T, GATED><<<grid, kDecThreads, smem, s>>>(q, k, v, g, o, state, n_units, dk, dv);
+    else
+        decode_scalar_kernel<T, GATED><<<grid, kDecThreads, smem, s>>>(q, k, v, g, o, state, n_units, dk, dv);
     return cudaGetLastError();
+}
+
+cudaError_t launch_decode(const void* q, const void* k, const void* v, const void* g, void* o, float* state,
+                          int dtype, int64_t n_units, int dk, int dv, int num_sms, cudaStream_t s) {
+    if (n_units <= 0) return cudaSuccess;
+    auto run = [&](auto elem) {
+        using T = decltype(elem);
+        const T *qq = static_cast<const T*>(q), *kk = static_cast<const T*>(k), *vv = static_cast<const T*>(v),
+                *gg = static_cast<const T*>(g);
+        T* oo = static_cast<T*>(o);
+        return gg ? launch_decode_t<T, true>(qq, kk, vv, gg, oo, state, n_units, dk, dv, num_sms, s)
+                  : launch_decode_t<T, false>(qq, kk, vv, gg, oo, state, n_units, dk, dv, num_sms, s);
+    };
+    return dtype == 0 ? run(float{}) : run(__nv_bfloat16{});
 }
 
 // S_0: copy of `src`, or zero.

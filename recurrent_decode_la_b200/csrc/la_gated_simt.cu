@@ -1,0 +1,455 @@
+// la_gated_simt.cu -- the gated recurrence and its gradient on the CUDA cores,
+// in fp32, for fp32 inputs and for the head sizes that the tensor-core kernels
+// do not take.  The formulas stand in la_gated.h; chunks of 32 tokens.
+//
+// Bound by fp32 FMAs: at d_k = d_v = 128 the chunk phase of the gradient does
+// about 5 x 128 x 128 x 2 + 5 x 32 x 128 x 2 flops a token for 7 x 128 x 4
+// bytes.  Each product keeps a 4 x 4 tile per thread: one warp owns four rows
+// (their operand is a broadcast), its lanes own columns lane + 32 m, so an
+// operand read along either of its dimensions is free of bank conflicts when
+// rows are 129 (33) floats apart.  Prefix sums of the gates are held in
+// float64: their differences, the exponents of the decays, stay exact to
+// fp32 however strong the gates are.
+#include <cuda_bf16.h>
+
+#include "la_gated.h"
+#include "la_internal.h"
+
+namespace la {
+namespace {
+
+constexpr int C = kGatedSimtChunk;
+constexpr int kLd = 129;   // row stride of [.][128] tiles
+constexpr int kLdC = 33;   // row stride of [C][C] tiles
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float ld1(const float* p, int64_t i) { return p[i]; }
+__device__ __forceinline__ float ld1(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
+__device__ __forceinline__ void st1(float* p, int64_t i, float x) { p[i] = x; }
+__device__ __forceinline__ void st1(__nv_bfloat16* p, int64_t i, float x) { p[i] = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ float decay(double x) { return exp2f(static_cast<float>(x * 1.4426950408889634)); }
+
+// Inclusive prefix sums of the chunk's log gates (one warp; rows >= nv add 0).
+template <typename T>
+__device__ __forceinline__ void gate_prefix(const GatedProblem& p, int64_t row0, int nv, double* G) {
+    const int lane = threadIdx.x & 31;
+    float x = 0.f;
+    if (p.g != nullptr && lane < nv) {
+        x = ld1(static_cast<const T*>(p.g), row0 + lane);
+        x = x < kGateFloor ? kGateFloor : x;
+    }
+    double s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    G[lane] = s;
+}
+
+// Rows row0 .. row0 + nv - 1 of x [.][d] into dst [C][kLd]; the rest zero.
+template <typename T>
+__device__ __forceinline__ void load_tile(float* dst, const void* x, int64_t row0, int nv, int d) {
+    const T* X = static_cast<const T*>(x) + row0 * d;
+    for (int i = threadIdx.x; i < C * 128; i += kThreads) {
+        const int r = i >> 7, c = i & 127;
+        dst[r * kLd + c] = (r < nv && c < d) ? ld1(X, static_cast<int64_t>(r) * d + c) : 0.f;
+    }
+}
+
+__device__ __forceinline__ void load_state(float* dst, const float* src, int dk, int dv) {
+    for (int i = threadIdx.x; i < 128 * 128; i += kThreads) {
+        const int r = i >> 7, c = i & 127;
+        dst[r * kLd + c] = (r < dk && c < dv) ? src[r * dv + c] : 0.f;
+    }
+}
+
+// acc[i][m] = sum_{k in [k0, k1)} a(4 w + i, k) b(k, lane + 32 m): 32 x 128 outputs over 8 warps.
+struct Acc {
+    float x[4][4];
+};
+__device__ __forceinline__ void zero(Acc& acc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc.x[i][m] = 0.f;
+}
+__device__ __forceinline__ void mm(Acc& acc, const float* a, int ai, int ak, const float* b, int bk, int bn, int K) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float* A = a + 4 * w * ai;
+    const float* B = b + lane * bn;
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+        float av[4], bv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[i] = A[i * ai + k * ak];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) bv[m] = B[k * bk + 32 * m * bn];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc.x[i][m] = fmaf(av[i], bv[m], acc.x[i][m]);
+    }
+}
+
+// dst[i][j] = a_i . b_j over K columns, 32 x 32 outputs over 8 warps (four rows each).
+__device__ __forceinline__ void scores(float (&acc)[4], const float* a, const float* b, int K) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+    for (int k = 0; k < K; ++k) {
+        const float y = b[lane * kLd + k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(a[(4 * w + i) * kLd + k], y, acc[i]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_rows(void* y, int64_t row0, int nv, int d, const Acc& acc) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    T* Y = static_cast<T*>(y) + row0 * d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int r = 4 * w + i, c = lane + 32 * m;
+            if (r < nv && c < d) st1(Y, static_cast<int64_t>(r) * d + c, acc.x[i][m]);
+        }
+}
+
+// ---------------------------------------------------------------------------
+// State phase.  One CTA owns 32 of the d_v columns of a unit's state (a state
+// column depends on no other), in registers, 4 x 4 per thread, and walks the
+// chunks.  Forward: X = K weighted by e^{G_C - G_j}, Y = V.  Reverse: X = Q
+// weighted by e^{G_i}, Y = dO.
+// ---------------------------------------------------------------------------
+template <typename T, bool REV>
+__global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const GatedProblem p, int col_blocks) {
+    __shared__ float X[C][132];
+    __shared__ float Y[C][32];
+    __shared__ double G[C];
+    const int tid = threadIdx.x;
+    const int64_t u = blockIdx.x / col_blocks;
+    const int c0 = static_cast<int>(blockIdx.x % col_blocks) * 32;
+    const GatedUnit un = gated_unit(p, u);
+    if (un.len == 0) return;
+    const int r0 = 4 * (tid >> 3), n0 = c0 + 4 * (tid & 7);
+    const int dk = p.dk, dv = p.dv;
+    const int64_t usz = static_cast<int64_t>(dk) * dv;
+    const float* in = REV ? p.dstate + u * usz : (p.state ? p.state + u * usz : (p.s0 ? p.s0 + u * usz : nullptr));
+    float* out = REV ? p.dstate + u * usz : (p.state ? p.state + u * usz : nullptr);
+    float* slots = static_cast<float*>(REV ? p.e_states : p.s_states);
+    float S[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            S[i][m] = (in && r0 + i < dk && n0 + m < dv) ? in[(r0 + i) * dv + n0 + m] : 0.f;
+    const T* xs = static_cast<const T*>(REV ? p.q : p.k);
+    const T* ys = static_cast<const T*>(REV ? p.d_o : p.v);
+    const int nch = (un.len + C - 1) / C;
+    for (int cc = 0; cc < nch; ++cc) {
+        const int c = REV ? nch - 1 - cc : cc;
+        const int nv = min(C, un.len - c * C);
+        const int64_t row0 = un.row0 + static_cast<int64_t>(c) * C;
+        float* slot = slots + (un.slot0 + c) * usz;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                if (r0 + i < dk && n0 + m < dv) slot[(r0 + i) * dv + n0 + m] = S[i][m];
+        __syncthreads();
+        if (tid < 32) gate_prefix<T>(p, row0, nv, G);
+        for (int i = tid; i < C * 32; i += kThreads) {
+            const int r = i >> 5, n = c0 + (i & 31);
+            Y[r][i & 31] = (r < nv && n < dv) ? ld1(ys, (row0 + r) * dv + n) : 0.f;
+        }
+        __syncthreads();
+        for (int i = tid; i < C * 128; i += kThreads) {
+            const int r = i >> 7, d = i & 127;
+            const float w = decay(REV ? G[r] : G[C - 1] - G[r]);
+            X[r][d] = (r < nv && d < dk) ? w * ld1(xs, (row0 + r) * dk + d) : 0.f;
+        }
+        const float gamma = decay(G[C - 1]);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) S[i][m] *= gamma;
+        for (int j = 0; j < nv; ++j) {
+            const float4 x = *reinterpret_cast<const float4*>(&X[j][r0]);
+            const float4 y = *reinterpret_cast<const float4*>(&Y[j][n0 - c0]);
+            const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) S[i][m] = fmaf(xv[i], yv[m], S[i][m]);
+        }
+    }
+    if (out) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                if (r0 + i < dk && n0 + m < dv) out[(r0 + i) * dv + n0 + m] = S[i][m];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Chunk phase of the prefill: one CTA per chunk.
+// ---------------------------------------------------------------------------
+constexpr size_t kOutSmem = sizeof(float) * (3 * C * kLd + 128 * kLd + C * kLdC) + sizeof(double) * C;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) gated_out_simt_kernel(const GatedProblem p) {
+    extern __shared__ double sm_d[];
+    double* G = sm_d;
+    float* Q = reinterpret_cast<float*>(G + C);
+    float* K = Q + C * kLd;
+    float* V = K + C * kLd;
+    float* S = V + C * kLd;
+    float* P = S + 128 * kLd;
+    const GatedChunk ch = gated_chunk(p, blockIdx.x, C);
+    if (ch.nv <= 0) return;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    if (tid < 32) gate_prefix<T>(p, ch.row0, ch.nv, G);
+    load_tile<T>(Q, p.q, ch.row0, ch.nv, p.dk);
+    load_tile<T>(K, p.k, ch.row0, ch.nv, p.dk);
+    load_tile<T>(V, p.v, ch.row0, ch.nv, p.dv);
+    load_state(S, static_cast<const float*>(p.s_states) + static_cast<int64_t>(blockIdx.x) * p.dk * p.dv, p.dk, p.dv);
+    __syncthreads();
+    float a[4];
+    scores(a, Q, K, p.dk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * w + i;
+        P[r * kLdC + lane] = lane <= r ? a[i] * decay(G[r] - G[lane]) : 0.f;
+    }
+    Acc acc;
+    zero(acc);
+    mm(acc, Q, kLd, 1, S, kLd, 1, p.dk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f = decay(G[4 * w + i]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc.x[i][m] *= f;
+    }
+    __syncwarp();  // a warp reads the rows of P that it wrote
+    mm(acc, P, kLdC, 1, V, kLd, 1, min(4 * w + 4, ch.nv));  // rows 4w..4w+3 read keys up to 4w+3
+    store_rows<T>(p.o, ch.row0, ch.nv, p.dv, acc);
+}
+
+// ---------------------------------------------------------------------------
+// Chunk phase of the gradient: one CTA per chunk.
+// ---------------------------------------------------------------------------
+constexpr size_t kGradSmem =
+    sizeof(float) * (4 * C * kLd + 2 * 128 * kLd + 2 * C * kLdC + 2 * C + 8) + sizeof(double) * C;
+
+__device__ __forceinline__ float row_dot(const float (&x)[4], const float* y) {
+    const int lane = threadIdx.x & 31;
+    float s = 0.f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) s = fmaf(x[m], y[lane + 32 * m], s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) gated_grad_simt_kernel(const GatedProblem p) {
+    extern __shared__ double sm_d[];
+    double* G = sm_d;
+    float* Q = reinterpret_cast<float*>(G + C);
+    float* K = Q + C * kLd;
+    float* V = K + C * kLd;
+    float* DO = V + C * kLd;
+    float* S = DO + C * kLd;
+    float* E = S + 128 * kLd;
+    float* W = E + 128 * kLd;   // w_ij (do_i . v_j), later M
+    float* P = W + C * kLdC;    // w_ij (q_i . k_j)
+    float* ri = P + C * kLdC;   // e^{G_i} q_i . (S do_i)
+    float* cj = ri + C;         // e^{G_C - G_j} k_j . (E v_j)
+    float* es = cj + C;         // per-warp sums of <E, S>
+    const GatedChunk ch = gated_chunk(p, blockIdx.x, C);
+    if (ch.nv <= 0) return;
+    const int nv = ch.nv, dk = p.dk, dv = p.dv;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int64_t usz = static_cast<int64_t>(dk) * dv;
+    if (tid < 32) gate_prefix<T>(p, ch.row0, nv, G);
+    load_tile<T>(Q, p.q, ch.row0, nv, dk);
+    load_tile<T>(K, p.k, ch.row0, nv, dk);
+    load_tile<T>(V, p.v, ch.row0, nv, dv);
+    load_tile<T>(DO, p.d_o, ch.row0, nv, dv);
+    load_state(S, static_cast<const float*>(p.s_states) + blockIdx.x * usz, dk, dv);
+    load_state(E, static_cast<const float*>(p.e_states) + blockIdx.x * usz, dk, dv);
+    __syncthreads();
+    float a[4], b[4];
+    scores(a, Q, K, dk);
+    scores(b, DO, V, dv);
+    float mij[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * w + i;
+        const float wij = lane <= r ? decay(G[r] - G[lane]) : 0.f;
+        P[r * kLdC + lane] = lane <= r ? wij * a[i] : 0.f;
+        W[r * kLdC + lane] = lane <= r ? wij * b[i] : 0.f;
+        mij[i] = lane < r ? wij * a[i] * b[i] : 0.f;
+    }
+    float part = 0.f;
+    for (int i = tid; i < dk * 128; i += kThreads) {
+        const int r = i >> 7, c = i & 127;
+        part = fmaf(S[r * kLd + c], E[r * kLd + c], part);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0) es[w] = part;
+    __syncthreads();
+    Acc acc;
+    // dq
+    zero(acc);
+    mm(acc, DO, kLd, 1, S, 1, kLd, dv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * w + i;
+        const float f = decay(G[r]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc.x[i][m] *= f;
+        const float s = row_dot(acc.x[i], Q + r * kLd);
+        if (lane == 0) ri[r] = s;
+    }
+    mm(acc, W, kLdC, 1, K, kLd, 1, min(4 * w + 4, nv));
+    store_rows<T>(p.dq, ch.row0, nv, dk, acc);
+    // dk
+    zero(acc);
+    mm(acc, V, kLd, 1, E, 1, kLd, dv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * w + i;
+        const float f = decay(G[C - 1] - G[r]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc.x[i][m] *= f;
+        const float s = row_dot(acc.x[i], K + r * kLd);
+        if (lane == 0) cj[r] = s;
+    }
+    mm(acc, W, 1, kLdC, Q, kLd, 1, nv);
+    store_rows<T>(p.dk_, ch.row0, nv, dk, acc);
+    // dv
+    zero(acc);
+    mm(acc, K, kLd, 1, E, kLd, 1, dk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f = decay(G[C - 1] - G[4 * w + i]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) acc.x[i][m] *= f;
+    }
+    mm(acc, P, 1, kLdC, DO, kLd, 1, nv);
+    store_rows<T>(p.dv_, ch.row0, nv, dv, acc);
+    if (p.dg == nullptr) return;
+    __syncthreads();  // every warp is done with W
+#pragma unroll
+    for (int i = 0; i < 4; ++i) W[(4 * w + i) * kLdC + lane] = mij[i];
+    __syncthreads();
+    // dg_t: warp w takes t = w, w + 8, ..; lane j sums column j over i >= t
+    for (int t = w; t < nv; t += 8) {
+        float s = 0.f;
+        if (lane < t) {
+            s = cj[lane];
+            for (int i = t; i < nv; ++i) s += W[i * kLdC + lane];
+        } else if (lane < nv) {
+            s = ri[lane];
+        }
+        if (lane < 8) s = fmaf(decay(G[C - 1]), es[lane], s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) st1(static_cast<T*>(p.dg), ch.row0 + t, s);
+    }
+}
+
+__global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __restrict__ cu, int num_seqs, int64_t rows,
+                                                             int chunk, int32_t* __restrict__ choff) {
+    __shared__ int64_t warp_sum[32];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    int64_t before = 0;
+    for (int n0 = 0; n0 < num_seqs; n0 += 1024) {
+        const int n = n0 + tid;
+        int32_t x = 0;
+        if (n < num_seqs) {
+            const int a = cu[n], b = cu[n + 1];
+            if (!(a < 0 || b < a || static_cast<int64_t>(b) > rows)) x = (b - a + chunk - 1) / chunk;
+        }
+        int64_t s = x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        if (lane == 31) warp_sum[w] = s;
+        __syncthreads();
+        int64_t base = before, all = 0;
+        for (int i = 0; i < 32; ++i) {
+            if (i < w) base += warp_sum[i];
+            all += warp_sum[i];
+        }
+        if (n < num_seqs) choff[n] = static_cast<int32_t>(min(base + s - x, static_cast<int64_t>(0x7fffffff)));
+        before += all;
+        __syncthreads();
+    }
+    if (tid == 0) choff[num_seqs] = static_cast<int32_t>(min(before, static_cast<int64_t>(0x7fffffff)));
+}
+
+template <typename F>
+cudaError_t raise_smem(PerDeviceOnce& once, F kern, size_t bytes) {
+    return once.run([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    });
+}
+
+template <typename T>
+cudaError_t states_t(const GatedProblem& p, bool reverse, cudaStream_t s) {
+    const int cb = (p.dv + 31) / 32;
+    const int64_t grid = p.n_units * cb;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (reverse)
+        gated_states_simt_kernel<T, true><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p, cb);
+    else
+        gated_states_simt_kernel<T, false><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p, cb);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t out_t(const GatedProblem& p, cudaStream_t s) {
+    static PerDeviceOnce once;
+    cudaError_t e = raise_smem(once, gated_out_simt_kernel<T>, kOutSmem);
+    if (e != cudaSuccess) return e;
+    gated_out_simt_kernel<T><<<static_cast<unsigned>(p.groups * p.nc), kThreads, kOutSmem, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t grad_t(const GatedProblem& p, cudaStream_t s) {
+    static PerDeviceOnce once;
+    cudaError_t e = raise_smem(once, gated_grad_simt_kernel<T>, kGradSmem);
+    if (e != cudaSuccess) return e;
+    gated_grad_simt_kernel<T><<<static_cast<unsigned>(p.groups * p.nc), kThreads, kGradSmem, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, int chunk, int32_t* choff,
+                                 cudaStream_t s) {
+    chunk_offsets_kernel<<<1, 1024, 0, s>>>(cu, num_seqs, rows, chunk, choff);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gated_states_simt(const GatedProblem& p, bool reverse, cudaStream_t s) {
+    return p.dtype ? states_t<__nv_bfloat16>(p, reverse, s) : states_t<float>(p, reverse, s);
+}
+cudaError_t launch_gated_out_simt(const GatedProblem& p, cudaStream_t s) {
+    return p.dtype ? out_t<__nv_bfloat16>(p, s) : out_t<float>(p, s);
+}
+cudaError_t launch_gated_grad_simt(const GatedProblem& p, cudaStream_t s) {
+    return p.dtype ? grad_t<__nv_bfloat16>(p, s) : grad_t<float>(p, s);
+}
+
+}  // namespace la

@@ -33,6 +33,14 @@ struct Tuning {
 };
 const Tuning& tuning();
 
+// Host helpers shared by the entry points (la_api.cu).
+int current_sm_count();                    // SMs of the current device
+int cuda_fail_status(cudaError_t e);       // keeps the text for la_last_cuda_error(); LA_ERR_CUDA
+void set_last_error(const char* text);     // the same for a failure that is no cudaError_t
+// 3-D bf16 view (d, rows, groups) of a [groups][rows][d] tensor, box
+// (64, chunk, 1), 128-byte swizzle: one box fills one swizzled smem panel.
+bool encode_bf16_map(CUtensorMap* map, const void* base, int d, int64_t rows, int64_t groups, int chunk);
+
 // Per-device one-time set-up of a kernel's attributes (a raised shared-memory
 // limit and the like).  cudaFuncSetAttribute may not run inside a stream
 // capture, so the first launch on each device (made outside any capture)
@@ -82,6 +90,7 @@ struct PrefillProblem {
     const void* q;
     const void* k;
     const void* v;
+    const void* g;  // log gates [groups][rows] (few-token kernel only; nullptr: no decay)
     void* o;
     float* state;
     int dtype;  // 0 = f32, 1 = bf16
@@ -158,7 +167,8 @@ constexpr int kMaxOrderedSeqs = 4096;
 cudaError_t launch_length_order(const int32_t* cu, int num_seqs, int64_t total_rows, int32_t* order,
                                 cudaStream_t s);
 
-cudaError_t launch_decode(const void* q, const void* k, const void* v, void* o, float* state,
+// g: one log gate a unit, or nullptr (no decay).
+cudaError_t launch_decode(const void* q, const void* k, const void* v, const void* g, void* o, float* state,
                           int dtype, int64_t n_units, int dk, int dv, int num_sms,
                           cudaStream_t s);
 

@@ -23,6 +23,10 @@
 // S[r] += k_t[r] v_t, then o_t's partial += q_t[r] S[r], and it writes the
 // final row straight back.  The partials of the rows are summed by warp
 // shuffles, then across warps in shared memory.  All arithmetic is fp32.
+//
+// With log gates the recurrence is S_t = e^{g_t} S_{t-1} + k_t v_t^T: each
+// thread takes the decays of its unit from shared memory and multiplies the
+// row before it adds (GATED), half as many FP operations again.
 #include <cuda_bf16.h>
 
 #include "la_device.cuh"
@@ -83,6 +87,13 @@ __device__ __forceinline__ void elem_out4<__nv_bfloat16>(__nv_bfloat16* p, float
     }
 }
 
+// a *= s
+__device__ __forceinline__ void mul4(float4& a, float s) {
+    const float2 ss = make_float2(s, s);
+    const float2 lo = __fmul2_rn(ss, make_float2(a.x, a.y)), hi = __fmul2_rn(ss, make_float2(a.z, a.w));
+    a = make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+
 // a += s * b, as two paired fp32 FMAs (sm_100)
 __device__ __forceinline__ void fma4(float4& a, float s, const float4& b) {
     const float2 ss = make_float2(s, s);
@@ -93,10 +104,10 @@ __device__ __forceinline__ void fma4(float4& a, float s, const float4& b) {
 
 // Shared memory (floats) of one CTA: the CTA's state tile [d_k][ncol], q
 // and k transposed [d_k][TM] (a row's tokens are contiguous), v [TM][ncol],
-// per-warp partial outputs [warps][TM][ncol].
+// per-warp partial outputs [warps][TM][ncol], the tokens' decays [TM].
 __host__ __device__ constexpr size_t short_smem_floats(int tm, int dk, int ncol, int warps) {
     return static_cast<size_t>(dk) * ncol + 2 * static_cast<size_t>(dk) * tm +
-           static_cast<size_t>(tm) * (1 + warps) * ncol;
+           static_cast<size_t>(tm) * (1 + warps) * ncol + tm;
 }
 
 // Bring the 128-byte line holding p into L2 (a hint: no data is returned).
@@ -148,9 +159,9 @@ __device__ __forceinline__ void short_prefetch_tokens(const PrefillProblem& p, i
 // change nothing); the final row goes straight back to global memory.
 // St / Sg: this CTA's state tile in shared / global memory, row r, this
 // thread's four columns 4*c4 .. 4*c4+3.
-template <int TM>
+template <int TM, bool GATED>
 __device__ __forceinline__ void short_row(const float* St, float* Sg, int r, int ncol, int dv, int c4,
-                                          const float* qT, const float* kT, const float4 (&vv)[TM],
+                                          const float* qT, const float* kT, const float* at, const float4 (&vv)[TM],
                                           float4 (&acc)[TM]) {
     float4 s = reinterpret_cast<const float4*>(St + r * ncol)[c4];
     const float4* q4 = reinterpret_cast<const float4*>(qT + r * TM);
@@ -158,12 +169,17 @@ __device__ __forceinline__ void short_row(const float* St, float* Sg, int r, int
 #pragma unroll
     for (int t4 = 0; t4 < TM / 4; ++t4) {
         const float4 kk = k4[t4], qq = q4[t4];
+        const float4 aa = GATED ? reinterpret_cast<const float4*>(at)[t4] : make_float4(1.f, 1.f, 1.f, 1.f);
+        if (GATED) mul4(s, aa.x);
         fma4(s, kk.x, vv[4 * t4 + 0]);
         fma4(acc[4 * t4 + 0], qq.x, s);
+        if (GATED) mul4(s, aa.y);
         fma4(s, kk.y, vv[4 * t4 + 1]);
         fma4(acc[4 * t4 + 1], qq.y, s);
+        if (GATED) mul4(s, aa.z);
         fma4(s, kk.z, vv[4 * t4 + 2]);
         fma4(acc[4 * t4 + 2], qq.z, s);
+        if (GATED) mul4(s, aa.w);
         fma4(s, kk.w, vv[4 * t4 + 3]);
         fma4(acc[4 * t4 + 3], qq.w, s);
     }
@@ -204,7 +220,7 @@ __device__ __forceinline__ void short_reduce_store(float4 (&acc)[TM], float* red
     }
 }
 
-template <typename E, int TM, int NT>
+template <typename E, int TM, int NT, bool GATED>
 __global__ void __launch_bounds__(NT, (TM <= 8 ? 2 : 1) * (kShortThreadsMax / NT))
     prefill_short_kernel(const PrefillProblem p, int cb_count) {
     extern __shared__ float4 sm4[];
@@ -244,6 +260,7 @@ __global__ void __launch_bounds__(NT, (TM <= 8 ? 2 : 1) * (kShortThreadsMax / NT
     float* kT = qT + dk * TM;         // [dk][TM]
     float* vs = kT + dk * TM;         // [TM][ncol]
     float* red = vs + TM * ncol;      // [NT / 32][TM][ncol]
+    float* at = red + (NT / 32) * TM * ncol;  // [TM] e^{g_t} (16-byte aligned: ncol is a multiple of 4)
     const int64_t rbase = un.rbase;
     const E* Q = static_cast<const E*>(p.q) + rbase * dk;
     const E* K = static_cast<const E*>(p.k) + rbase * dk;
@@ -253,6 +270,7 @@ __global__ void __launch_bounds__(NT, (TM <= 8 ? 2 : 1) * (kShortThreadsMax / NT
     // the token loads first (d_k, d_v <= 128: at most TM * 128 / NT
     // elements of each per thread), in registers until the state copies are
     // issued
+    const float gt = GATED && tid < len ? elem_in<E>(static_cast<const E*>(p.g), rbase + tid) : 0.f;
     constexpr int kPer = (TM * 128 + NT - 1) / NT;
     float qv[kPer], kv[kPer], vt[kPer];
 #pragma unroll
@@ -288,6 +306,7 @@ __global__ void __launch_bounds__(NT, (TM <= 8 ? 2 : 1) * (kShortThreadsMax / NT
         }
         if (i < TM * ncol) vs[i] = vt[j];
     }
+    if (GATED && tid < TM) at[tid] = expf(gt);
     __syncthreads();
     float4 vv[TM];
 #pragma unroll
@@ -299,10 +318,10 @@ __global__ void __launch_bounds__(NT, (TM <= 8 ? 2 : 1) * (kShortThreadsMax / NT
     for (int t = 0; t < TM; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll 1
-    for (int i = 0; i < nh; ++i) short_row<TM>(St, Sg, r0 + i * rpp, ncol, dv, c4, qT, kT, vv, acc);
+    for (int i = 0; i < nh; ++i) short_row<TM, GATED>(St, Sg, r0 + i * rpp, ncol, dv, c4, qT, kT, at, vv, acc);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll 1
-    for (int i = nh; i < nrow; ++i) short_row<TM>(St, Sg, r0 + i * rpp, ncol, dv, c4, qT, kT, vv, acc);
+    for (int i = nh; i < nrow; ++i) short_row<TM, GATED>(St, Sg, r0 + i * rpp, ncol, dv, c4, qT, kT, at, vv, acc);
     short_reduce_store<E, TM, NT>(acc, red, ncol, cols4, len, O, dv, cbeg);
 }
 
@@ -322,9 +341,9 @@ int short_col_blocks(int64_t n_units, int num_sms, int dv, int nt) {
     return cb;
 }
 
-template <typename E, int TM, int NT>
+template <typename E, int TM, int NT, bool GATED>
 cudaError_t launch_short_tm(const PrefillProblem& p, int cb, cudaStream_t s) {
-    auto kern = prefill_short_kernel<E, TM, NT>;
+    auto kern = prefill_short_kernel<E, TM, NT, GATED>;
     const size_t smem = short_smem_floats(TM, p.dk, p.dv / cb, NT / 32) * sizeof(float);
     // raise the limit to the largest this instantiation can ask for, once
     // per device (not inside a stream capture: the first launch sets it)
@@ -353,11 +372,16 @@ cudaError_t launch_short_tm(const PrefillProblem& p, int cb, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename E, int NT, bool GATED>
+cudaError_t launch_short_g(const PrefillProblem& p, int64_t max_tokens, int cb, cudaStream_t s) {
+    if (max_tokens <= 4) return launch_short_tm<E, 4, NT, GATED>(p, cb, s);
+    if (max_tokens <= 8) return launch_short_tm<E, 8, NT, GATED>(p, cb, s);
+    return launch_short_tm<E, 16, NT, GATED>(p, cb, s);
+}
+
 template <typename E, int NT>
 cudaError_t launch_short_t(const PrefillProblem& p, int64_t max_tokens, int cb, cudaStream_t s) {
-    if (max_tokens <= 4) return launch_short_tm<E, 4, NT>(p, cb, s);
-    if (max_tokens <= 8) return launch_short_tm<E, 8, NT>(p, cb, s);
-    return launch_short_tm<E, 16, NT>(p, cb, s);
+    return p.g ? launch_short_g<E, NT, true>(p, max_tokens, cb, s) : launch_short_g<E, NT, false>(p, max_tokens, cb, s);
 }
 
 }  // namespace

@@ -1,0 +1,167 @@
+// la_rotary.cu -- rotary positions of q and k, and the table of their
+// frequencies.
+//
+// Pair i of a head (elements i and i + rot/2, or 2i and 2i + 1) at position
+// pos turns by the angle pos * freq[i]:
+//     y_a = (x_a cos - x_b sin) * scale,   y_b = (x_b cos + x_a sin) * scale,
+// the inverse (also the gradient: the map is linear and orthogonal up to
+// `scale`) by the negated angle.  Elements rot .. d-1 pass unchanged.
+//
+// Bound by memory: each element is read once and written once.  The angle is
+// taken in float64, as a fraction of a turn whose whole turns are dropped, so
+// far positions lose nothing (a float32 product is off by a twentieth of a
+// radian at position 2^20); that costs about fifty instructions a pair, so a
+// thread takes V pairs (two 16-byte vectors) of one token and walks the heads
+// with them, q and k together.
+#include <cuda_bf16.h>
+
+#include "la_gated.h"
+#include "la_internal.h"
+
+namespace la {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    T x[V];
+};
+__device__ __forceinline__ float get(float x) { return x; }
+__device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float& y, float x) { y = x; }
+__device__ __forceinline__ void put(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+
+// Row t of the packed layout: its place in its sequence n (-1: in none).
+__device__ __forceinline__ int packed_place(const int32_t* cu, int num_seqs, int64_t t, int* seq) {
+    if (t < cu[0] || t >= cu[num_seqs]) return -1;
+    int lo = 0, hi = num_seqs - 1;  // the last sequence that begins at or before t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    *seq = lo;
+    return static_cast<int>(t - cu[lo]);
+}
+
+// One thread: V pairs (or V passed elements) of one token, heads h0 .. h0 + heads - 1 of both tensors.
+template <typename T, int V, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryProblem p, int items, int heads) {
+    const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
+    if (i >= p.B * p.T * items) return;
+    const int item = static_cast<int>(i % items);
+    const int64_t bt = i / items, b = bt / p.T, t = bt % p.T;
+    const int pair_items = p.rot / 2 / V;
+    const int64_t h0 = static_cast<int64_t>(blockIdx.y) * heads;
+    const int64_t h1 = h0 + heads < p.H ? h0 + heads : p.H;
+    int seq = static_cast<int>(b);
+    int64_t place = t;
+    if (p.cu != nullptr) {
+        place = packed_place(p.cu, p.num_seqs, t, &seq);
+        if (place < 0) return;
+    }
+    const int64_t step = p.T * p.d;  // between heads
+    const int64_t base = ((b * p.H + h0) * p.T + t) * p.d;
+    if (item >= pair_items) {  // passed through (nothing to do in place)
+        const int64_t at = base + p.rot + static_cast<int64_t>(item - pair_items) * V;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const T* x = static_cast<const T*>(p.x[which]);
+            T* y = static_cast<T*>(p.y[which]);
+            if (x == nullptr || x == y) continue;
+            for (int64_t h = 0; h < h1 - h0; ++h)
+                *reinterpret_cast<Vec<T, V>*>(y + at + h * step) = *reinterpret_cast<const Vec<T, V>*>(x + at + h * step);
+        }
+        return;
+    }
+    const int64_t pos = place + (p.start ? p.start[seq] : 0);
+    float c[V], s[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const double turns = static_cast<double>(pos) * (static_cast<double>(p.freq[item * V + e]) * 0.15915494309189535);
+        sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s[e], &c[e]);
+        c[e] *= p.scale;
+        s[e] *= p.inverse ? -p.scale : p.scale;
+    }
+    const int64_t a0 = base + (INTERLEAVED ? 2 * item * V : item * V);
+    const int64_t a1 = a0 + (INTERLEAVED ? V : p.rot / 2);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const T* x = static_cast<const T*>(p.x[which]);
+        T* y = static_cast<T*>(p.y[which]);
+        if (x == nullptr) continue;
+#pragma unroll 4
+        for (int64_t h = 0; h < h1 - h0; ++h) {
+            Vec<T, V> u = *reinterpret_cast<const Vec<T, V>*>(x + a0 + h * step);
+            Vec<T, V> w = *reinterpret_cast<const Vec<T, V>*>(x + a1 + h * step);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                // the pair's elements: (u[e], w[e]), or, interleaved, entries 2e and 2e + 1 of u followed by w
+                T& ra = INTERLEAVED ? (2 * e < V ? u.x[(2 * e) % V] : w.x[(2 * e) % V]) : u.x[e];
+                T& rb = INTERLEAVED ? (2 * e + 1 < V ? u.x[(2 * e + 1) % V] : w.x[(2 * e + 1) % V]) : w.x[e];
+                const float fa = get(ra), fb = get(rb);
+                put(ra, fa * c[e] - fb * s[e]);
+                put(rb, fb * c[e] + fa * s[e]);
+            }
+            *reinterpret_cast<Vec<T, V>*>(y + a0 + h * step) = u;
+            *reinterpret_cast<Vec<T, V>*>(y + a1 + h * step) = w;
+        }
+    }
+}
+
+template <typename T, int V>
+cudaError_t rotary_v(const RotaryProblem& p, int num_sms, cudaStream_t s) {
+    const int items = (p.rot / 2 + p.d - p.rot) / V;
+    const int64_t threads = p.B * p.T * items;
+    const int64_t blocks = (threads + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // few tokens: the heads are shared out over the grid until it covers the SMs
+    int64_t groups = (static_cast<int64_t>(num_sms) * 8 + blocks - 1) / blocks;
+    if (groups > p.H) groups = p.H;
+    if (groups > 65535) groups = 65535;
+    const int heads = static_cast<int>((p.H + groups - 1) / groups);
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((p.H + heads - 1) / heads));
+    if (p.interleaved)
+        rotary_kernel<T, V, true><<<grid, kThreads, 0, s>>>(p, items, heads);
+    else
+        rotary_kernel<T, V, false><<<grid, kThreads, 0, s>>>(p, items, heads);
+    return cudaGetLastError();
+}
+
+__global__ void rotary_init_kernel(float* freq, int rot, double base, int scaling, double factor, double original,
+                                   double beta_fast, double beta_slow) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= rot / 2) return;
+    if (scaling == 2 && rot > 2) base *= pow(factor, static_cast<double>(rot) / (rot - 2));
+    double f = pow(base, -2.0 * i / rot);
+    if (scaling == 1) f /= factor;
+    if (scaling == 3) {
+        // turns within the original length: many keep their frequency, few are stretched
+        const double turns = original * f / 6.283185307179586;
+        double keep = (turns - beta_slow) / (beta_fast - beta_slow);
+        keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+        f = f * keep + f / factor * (1.0 - keep);
+    }
+    freq[i] = static_cast<float>(f);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryProblem& p, int num_sms, cudaStream_t s) {
+    const int size = p.dtype ? 2 : 4, v = 16 / size;
+    uintptr_t bits = 0;
+    for (int w = 0; w < 2; ++w) bits |= reinterpret_cast<uintptr_t>(p.x[w]) | reinterpret_cast<uintptr_t>(p.y[w]);
+    // 16-byte accesses where every vector of a row is aligned and whole
+    const bool vec = bits % 16 == 0 && p.d % v == 0 && (p.rot / 2) % v == 0;
+    if (p.dtype) return vec ? rotary_v<__nv_bfloat16, 8>(p, num_sms, s) : rotary_v<__nv_bfloat16, 1>(p, num_sms, s);
+    return vec ? rotary_v<float, 4>(p, num_sms, s) : rotary_v<float, 1>(p, num_sms, s);
+}
+
+cudaError_t launch_rotary_init(float* freq, int rot, double base, int scaling, double factor, double original,
+                               double beta_fast, double beta_slow, cudaStream_t s) {
+    rotary_init_kernel<<<(rot / 2 + 127) / 128, 128, 0, s>>>(freq, rot, base, scaling, factor, original, beta_fast,
+                                                             beta_slow);
+    return cudaGetLastError();
+}
+
+}  // namespace la
