@@ -86,10 +86,10 @@ __device__ __forceinline__ GatedUnit gated_unit(const GatedProblem& p, int64_t u
 }
 
 struct GatedChunk {
-    int64_t row0;  // first row of the chunk; group = row0 / rows
-    int64_t unit;
-    int nv;  // its tokens; 0: the slot holds no chunk
-    int c;   // its place in the unit
+    int64_t row0;  // first row of the chunk in the [groups][rows] token layout
+    int group;
+    int row;  // row0 = group * rows + row
+    int nv;   // its tokens; 0: the slot holds no chunk
 };
 
 // The chunk of a workspace slot.
@@ -99,7 +99,7 @@ __device__ __forceinline__ GatedChunk gated_chunk(const GatedProblem& p, int64_t
     if (p.cu == nullptr) {
         const int64_t r = static_cast<int64_t>(ci) * C;
         const int64_t left = p.rows - r;
-        return {group * p.rows + r, group, static_cast<int>(left < C ? left : C), ci};
+        return {group * p.rows + r, static_cast<int>(group), static_cast<int>(r), static_cast<int>(left < C ? left : C)};
     }
     if (ci >= p.choff[p.num_seqs]) return {0, 0, 0, 0};
     int lo = 0, hi = p.num_seqs - 1;  // the last sequence with choff[n] <= ci
@@ -111,7 +111,7 @@ __device__ __forceinline__ GatedChunk gated_chunk(const GatedProblem& p, int64_t
     const int c = ci - p.choff[lo];
     const int64_t a = p.cu[lo] + static_cast<int64_t>(c) * C;
     const int64_t left = p.cu[lo + 1] - a;
-    return {group * p.rows + a, static_cast<int64_t>(lo) * p.H + group, static_cast<int>(left < C ? left : C), c};
+    return {group * p.rows + a, static_cast<int>(group), static_cast<int>(a), static_cast<int>(left < C ? left : C)};
 }
 
 // choff[n] = chunks of C tokens in the sequences before n (offsets out of
@@ -124,6 +124,19 @@ constexpr int kGatedSimtChunk = 32;
 cudaError_t launch_gated_states_simt(const GatedProblem& p, bool reverse, cudaStream_t s);
 cudaError_t launch_gated_out_simt(const GatedProblem& p, cudaStream_t s);
 cudaError_t launch_gated_grad_simt(const GatedProblem& p, cudaStream_t s);
+
+// Tensor-core kernels: bf16, d_k == d_v in {64, 128}, 16-byte aligned tensors;
+// chunks of 128 tokens, chunk states in bf16 as the swizzled shared-memory
+// image of the tile (two panels of 64 columns at d = 128).
+constexpr int kGatedTcChunk = 128;
+struct GatedMaps {
+    CUtensorMap q, k, v, d_o;       // loads: 64 columns x 128 rows
+    CUtensorMap o, dq, dk, dv;      // stores: 64 columns x 32 rows
+};
+// States at the chunk starts; with `grad` also the gradients at the chunk ends.
+cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s);
+cudaError_t launch_gated_out_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);
+cudaError_t launch_gated_grad_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);
 
 struct RotaryProblem {
     const void* x[2];  // q and k (k may be nullptr)

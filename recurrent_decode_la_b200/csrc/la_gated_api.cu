@@ -18,12 +18,13 @@ la_status refuse(la_status s, const char* why) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-enum Kernel { kNone, kShort, kSimt };
+enum Kernel { kNone, kShort, kTc, kSimt };
 
 // The kernels for these sizes.  max_tokens: T (dense) or max_seqlen (packed, 0: unknown).
 Kernel choose(la_dtype dtype, int64_t max_tokens, int dk, int dv, bool grad) {
     if (dk < 1 || dv < 1 || dk > 128 || dv > 128) return kNone;
     if (!grad && tuning().short_kernel && prefill_short_supported(max_tokens, dk, dv, nullptr)) return kShort;
+    if (dtype == LA_BF16 && dk == dv && (dk == 64 || dk == 128)) return kTc;
     return kSimt;
 }
 
@@ -38,10 +39,10 @@ struct Layout {
 Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs, bool grad) {
     Layout w;
     if (kind == kShort || kind == kNone) return w;
-    w.chunk = kGatedSimtChunk;
+    w.chunk = kind == kTc ? kGatedTcChunk : kGatedSimtChunk;
     // a packed sequence begins a chunk of its own
     w.nc = num_seqs > 0 ? T / w.chunk + num_seqs : (T + w.chunk - 1) / w.chunk;
-    const size_t states = up256(static_cast<size_t>(groups) * w.nc * dk * dv * sizeof(float));
+    const size_t states = up256(static_cast<size_t>(groups) * w.nc * dk * dv * (kind == kTc ? 2 : 4));
     w.s = num_seqs > 0 ? up256((static_cast<size_t>(num_seqs) + 1) * 4) : 0;
     w.e = w.s + states;
     w.bytes = w.e + (grad ? states : 0);
@@ -101,6 +102,23 @@ cudaError_t chunk_offsets(const GatedProblem& p, const Layout& w, cudaStream_t s
     return launch_chunk_offsets(p.cu, p.num_seqs, p.rows, w.chunk, const_cast<int32_t*>(p.choff), s);
 }
 
+// The tensor maps of the tensor-core kernels (every tensor 16-byte aligned).
+la_status maps(GatedMaps& m, const GatedProblem& p, bool grad) {
+    const void* all[] = {p.q, p.k, p.v, grad ? p.d_o : p.o, grad ? p.dq : p.q, grad ? p.dk_ : p.q, grad ? p.dv_ : p.q,
+                         grad ? p.dstate : p.state, p.s0};
+    for (const void* x : all)
+        if (!aligned16(x)) return refuse(LA_ERR_UNSUPPORTED, "bf16 with d 64 or 128 needs 16-byte aligned tensors");
+    const auto enc = [&](CUtensorMap& map, const void* x, int box_rows) {
+        return encode_bf16_map(&map, x, p.dk, p.rows, p.groups, box_rows);
+    };
+    bool ok = enc(m.q, p.q, kGatedTcChunk) && enc(m.k, p.k, kGatedTcChunk) && enc(m.v, p.v, kGatedTcChunk);
+    if (grad)
+        ok = ok && enc(m.d_o, p.d_o, kGatedTcChunk) && enc(m.dq, p.dq, 32) && enc(m.dk, p.dk_, 32) && enc(m.dv, p.dv_, 32);
+    else
+        ok = ok && enc(m.o, p.o, 32);
+    return ok ? LA_OK : refuse(LA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+}
+
 }  // namespace
 }  // namespace la
 
@@ -111,6 +129,7 @@ extern "C" {
 const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens, int d_k, int d_v) {
     switch (choose(dtype, max_tokens, d_k, d_v, false)) {
         case kShort: return "short";
+        case kTc: return "tc";
         case kSimt: return "simt";
         default: return "unsupported";
     }
@@ -152,6 +171,15 @@ la_status la_gated_prefill(const void* q, const void* k, const void* v, const vo
     const Layout w = plan(kind, p.groups, T, d_k, d_v, p.num_seqs, false);
     if ((st = place(p, w, workspace, workspace_bytes)) != LA_OK) return st;
     p.q = q; p.k = k; p.v = v; p.g = g; p.o = o; p.state = state;
+    if (kind == kTc) {
+        GatedMaps m = {};
+        if ((st = maps(m, p, false)) != LA_OK) return st;
+        const int sms = current_sm_count();
+        e = chunk_offsets(p, w, s);
+        if (e == cudaSuccess) e = launch_gated_states_tc(p, m, false, sms, s);
+        if (e == cudaSuccess) e = launch_gated_out_tc(p, m, sms, s);
+        return e == cudaSuccess ? LA_OK : fail(e);
+    }
     e = chunk_offsets(p, w, s);
     if (e == cudaSuccess) e = launch_gated_states_simt(p, false, s);
     if (e == cudaSuccess) e = launch_gated_out_simt(p, s);
@@ -177,7 +205,17 @@ la_status la_gated_prefill_backward(const void* q, const void* k, const void* v,
     p.dstate = dstate;
     p.dq = dq; p.dk_ = dk; p.dv_ = dv; p.dg = dg;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = chunk_offsets(p, w, s);
+    cudaError_t e;
+    if (kind == kTc) {
+        GatedMaps m = {};
+        if ((st = maps(m, p, true)) != LA_OK) return st;
+        const int sms = current_sm_count();
+        e = chunk_offsets(p, w, s);
+        if (e == cudaSuccess) e = launch_gated_states_tc(p, m, true, sms, s);
+        if (e == cudaSuccess) e = launch_gated_grad_tc(p, m, sms, s);
+        return e == cudaSuccess ? LA_OK : fail(e);
+    }
+    e = chunk_offsets(p, w, s);
     if (e == cudaSuccess) e = launch_gated_states_simt(p, false, s);
     if (e == cudaSuccess) e = launch_gated_states_simt(p, true, s);
     if (e == cudaSuccess) e = launch_gated_grad_simt(p, s);

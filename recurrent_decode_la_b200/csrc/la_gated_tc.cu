@@ -1,0 +1,1324 @@
+// la_gated_tc.cu -- the gated recurrence and its gradient on the tensor cores
+// (bf16, d_k == d_v == D in {64, 128}, chunks of 128 tokens).  The formulas
+// stand in la_gated.h.
+//
+// Three kernels.  gated_states_tc walks the chunks of a unit and writes the
+// state at every chunk's start (and, for the gradient, in reverse the gradient
+// of the state at every chunk's end); it is the only serial part, and its
+// per-chunk product needs no earlier state, so the chain is one multiply-add
+// per element and chunk.  gated_out_tc and gated_grad_tc then take all chunks
+// in any order, one at a time per SM.
+//
+// All three are bound by memory traffic.  Per 128 tokens at D = 128 the states
+// cost 96 KB (K and V read, a bf16 state written), the output 160 KB, the
+// gradient 288 KB, against the least possible 128 KB forward and 224 KB
+// backward.
+//
+// Rounding.  Sums, states and decays are fp32.  An operand of a product is
+// rounded to bf16 once where its result is bf16 too (decayed scores, chunk
+// states).  Where the result is an fp32 state, the decayed keys (queries) are
+// kept as the sum of two bf16 numbers, 2^-16 of them, at the price of a second
+// product.  A row's decay is applied to the fp32 accumulator, not to a bf16
+// operand.  The tensor core drops bits when it adds to an accumulator: a state
+// summed there over 8192 tokens is off by 9e-6 of itself, so the states live in
+// registers and an accumulator spans one chunk only.
+//
+// Waits are bounded: on expiry the kernel records the device error word, every
+// role winds down, copies and products in flight are drained (bounded), tensor
+// memory is freed and the kernel returns.
+#include "la_device.cuh"
+#include "la_gated.h"
+#include "la_internal.h"
+
+namespace la {
+namespace {
+
+constexpr int C = kGatedTcChunk;
+constexpr int kPanel = C * 128;  // 64 bf16 columns of a [128][D] tile
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four log gates (times log2 e) of this lane, tokens 4 lane .. 4 lane + 3 of
+// the chunk at row0; tokens at nv and behind decay by nothing.
+__device__ __forceinline__ void load_gates(const GatedProblem& p, int64_t row0, int nv, float (&x)[4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float v = 0.f;
+        if (p.g != nullptr && 4 * lane + e < nv)
+            v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.g)[row0 + 4 * lane + e]);
+        v = v < kGateFloor ? kGateFloor : v;
+        x[e] = v * kLog2e;
+    }
+}
+
+// Inclusive prefix sums over the 128 tokens.
+__device__ __forceinline__ void scan_up(const float (&x)[4], float (&G)[4]) {
+    const int lane = threadIdx.x & 31;
+    G[0] = x[0];
+#pragma unroll
+    for (int e = 1; e < 4; ++e) G[e] = G[e - 1] + x[e];
+    float s = G[3];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    float before = __shfl_up_sync(0xffffffffu, s, 1);
+    if (lane == 0) before = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) G[e] += before;
+}
+
+// Sums over the tokens behind each one (exclusive suffix sums); all = total.
+__device__ __forceinline__ void scan_down(const float (&x)[4], float (&B)[4], float& all) {
+    const int lane = threadIdx.x & 31;
+    B[3] = 0.f;
+#pragma unroll
+    for (int e = 2; e >= 0; --e) B[e] = B[e + 1] + x[e + 1];
+    float s = B[0] + x[0];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, s, o);
+        if (lane + o < 32) s += y;
+    }
+    float behind = __shfl_down_sync(0xffffffffu, s, 1);
+    if (lane == 31) behind = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) B[e] += behind;
+    all = __shfl_sync(0xffffffffu, s, 0);
+}
+
+// Zero rows nv .. 127 of a [128][D] tile (one warp).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int nv) {
+    const int n = (C - nv) * (D / 8);
+    for (int i = threadIdx.x & 31; i < n; i += 32) {
+        const int row = nv + i / (D / 8), ch = i % (D / 8);
+        st_shared_v4(tile + (ch >> 3) * kPanel + row * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
+    }
+}
+
+// 64 fp32 values of a row -> bf16 into a 128-byte swizzled panel row.
+__device__ __forceinline__ void put_row32(uint32_t panel, int row, int chunk0, const float (&x)[32]) {
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+        st_shared_v4(panel + sw128_off(row, chunk0 + ch), pack_bf16x2(x[8 * ch], x[8 * ch + 1]),
+                     pack_bf16x2(x[8 * ch + 2], x[8 * ch + 3]), pack_bf16x2(x[8 * ch + 4], x[8 * ch + 5]),
+                     pack_bf16x2(x[8 * ch + 6], x[8 * ch + 7]));
+}
+
+__device__ __forceinline__ void ld32f(uint32_t taddr, float (&x)[32]) {
+    uint32_t r[32];
+    tmem_ld32(taddr, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        asm volatile("" : "+r"(r[i]));  // not used before the wait
+        x[i] = __uint_as_float(r[i]);
+    }
+}
+
+__device__ __forceinline__ uint32_t tile_k(uint32_t tile, int ks, uint32_t panel) {  // K-major step ks
+    return tile + (ks >> 2) * panel + (ks & 3) * 32;
+}
+
+// ---------------------------------------------------------------------------
+// States.  Work item i < n_units: unit i forward, X = K, Y = V; the others
+// (gradient): unit i - n_units in reverse, X = Q, Y = dO.  Per chunk
+//     U = X'^T Y (X' = the decayed rows, as a high and a low bf16 part),
+//     S = gamma S + U.
+//   warp 0       TMA producer        warp 1  MMA issuer
+//   warp 2       decays of the chunk's tokens
+//   warps 4-7    X -> high part in place, low part beside it
+//   warps 8-15   (8-11 at D = 64) the state, 64 columns of a row per thread
+// ---------------------------------------------------------------------------
+template <int D>
+struct StCfg {
+    static constexpr int kThreads = 512;
+    static constexpr int NPAN = D / 64;
+    static constexpr int TILE = C * D * 2;
+    static constexpr int STAGE = 3 * TILE;  // X (then its high part), Y, low part of X
+    static constexpr int NS = D == 128 ? 2 : 4;
+    static constexpr int SB = D * D * 2, SB_PANEL = D * 128;
+    static constexpr int kGam = 8;  // live gammas: NS + 2 chunks at most
+    static constexpr int OFF_SB = NS * STAGE;
+    static constexpr int OFF_W = OFF_SB + SB;
+    static constexpr int OFF_GAM = OFF_W + NS * C * 4;
+    static constexpr int OFF_BAR = OFF_GAM + kGam * 4;
+    static constexpr int B_FULL = 0, B_EMPTY = NS, B_GFULL = 2 * NS, B_SCALED = 3 * NS, B_UFULL = 4 * NS,
+                         B_UEMPTY = 4 * NS + 2, B_DONE = 4 * NS + 4, NBAR = 4 * NS + 5;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int TM_COLS = 2 * D;
+    static_assert(SMEM <= 232448 && NS + 2 <= kGam, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(512, 1)
+    gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items) {
+    using Cfg = StCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+    float* wts = reinterpret_cast<float*>(smem + Cfg::OFF_W);
+    float* gam = reinterpret_cast<float*>(smem + Cfg::OFF_GAM);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t tmo = p.timeout_ns;
+    const uint32_t sbase = smem_u32(smem);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::NS; ++s) {
+            mbar_init(&bar[Cfg::B_FULL + s], 1);
+            mbar_init(&bar[Cfg::B_EMPTY + s], 1);
+            mbar_init(&bar[Cfg::B_GFULL + s], 1);
+            mbar_init(&bar[Cfg::B_SCALED + s], 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bar[Cfg::B_UFULL + b], 1);
+            mbar_init(&bar[Cfg::B_UEMPTY + b], 4 * Cfg::NPAN);
+        }
+        mbar_init(&bar[Cfg::B_DONE], 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Cfg::TM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // Calls f(unit, chunk, rows of it, global chunk number) for every chunk of this CTA's items, until f gives up.
+    auto walk = [&](auto&& f) -> bool {
+        int64_t g = 0;
+        for (int64_t i = blockIdx.x; i < n_items; i += gridDim.x) {
+            const bool rev = i >= p.n_units;
+            const GatedUnit un = gated_unit(p, rev ? i - p.n_units : i);
+            const int nch = (un.len + C - 1) / C;
+            for (int cc = 0; cc < nch; ++cc, ++g) {
+                const int c = rev ? nch - 1 - cc : cc;
+                if (!f(un, rev, c, min(C, un.len - c * C), g)) return false;
+            }
+        }
+        return true;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int64_t started = 0;
+            auto coords = [&](const GatedUnit& un, int c, int& row, int& group) {
+                const int64_t r = un.row0 + static_cast<int64_t>(c) * C;
+                group = static_cast<int>(un.row0 / p.rows);
+                row = static_cast<int>(r - group * p.rows);
+            };
+            const bool ok = walk([&](const GatedUnit& un, bool rev, int c, int, int64_t g) {
+                const int s = static_cast<int>(g % Cfg::NS);
+                if (g >= Cfg::NS &&
+                    !mbar_wait(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x600 + s))
+                    return false;
+                const CUtensorMap* mx = rev ? &m.q : &m.k;
+                const CUtensorMap* my = rev ? &m.d_o : &m.v;
+                int row, group;
+                coords(un, c, row, group);
+                mbar_arrive_expect_tx(&bar[Cfg::B_FULL + s], 2 * Cfg::TILE);
+                uint8_t* st = smem + s * Cfg::STAGE;
+#pragma unroll
+                for (int pn = 0; pn < Cfg::NPAN; ++pn) {
+                    tma_load_3d(st + pn * kPanel, mx, &bar[Cfg::B_FULL + s], pn * 64, row, group);
+                    tma_load_3d(st + Cfg::TILE + pn * kPanel, my, &bar[Cfg::B_FULL + s], pn * 64, row, group);
+                }
+                started = g + 1;
+                const int c2 = rev ? c - 1 : c + 1;
+                if (c2 >= 0 && c2 * C < un.len) {
+                    coords(un, c2, row, group);
+#pragma unroll
+                    for (int pn = 0; pn < Cfg::NPAN; ++pn) {
+                        tma_prefetch_l2_3d(mx, pn * 64, row, group);
+                        tma_prefetch_l2_3d(my, pn * 64, row, group);
+                    }
+                }
+                return true;
+            });
+            if (!ok || *abort_flag)
+                for (int64_t g = started > Cfg::NS ? started - Cfg::NS : 0; g < started; ++g)
+                    mbar_wait_drain(&bar[Cfg::B_FULL + g % Cfg::NS], (g / Cfg::NS) & 1, tmo);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t kId = idesc_bf16_f32(D, D, true, true);
+            bool issued = false;
+            walk([&](const GatedUnit&, bool, int, int, int64_t g) {
+                const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
+                if (!mbar_wait(&bar[Cfg::B_SCALED + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x610 + s)) return false;
+                if (g >= 2 && !mbar_wait(&bar[Cfg::B_UEMPTY + b], ((g >> 1) + 1) & 1, abort_flag, tmo, 0x618 + b))
+                    return false;
+                tc_fence_after();
+                const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE, lo = y + Cfg::TILE;
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+                    mma_bf16_ss(tmem + b * D, sdesc_sw128(lo + ks * 2048, kPanel, 1024),
+                                sdesc_sw128(y + ks * 2048, kPanel, 1024), kId, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+                    mma_bf16_ss(tmem + b * D, sdesc_sw128(x + ks * 2048, kPanel, 1024),
+                                sdesc_sw128(y + ks * 2048, kPanel, 1024), kId, 1);
+                mma_commit(&bar[Cfg::B_EMPTY + s]);
+                mma_commit(&bar[Cfg::B_UFULL + b]);
+                issued = true;
+                return true;
+            });
+            if (issued) {
+                mma_commit(&bar[Cfg::B_DONE]);
+                mbar_wait_drain(&bar[Cfg::B_DONE], 0, tmo);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        walk([&](const GatedUnit& un, bool rev, int c, int nv, int64_t g) {
+            const int s = static_cast<int>(g % Cfg::NS);
+            float x[4], w[4], all;
+            load_gates(p, un.row0 + static_cast<int64_t>(c) * C, nv, x);
+            if (rev) {
+                scan_up(x, w);
+                all = __shfl_sync(0xffffffffu, w[3], 31);
+            } else {
+                scan_down(x, w, all);
+            }
+            if (g >= Cfg::NS &&
+                !mbar_wait_warp(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x620 + s))
+                return false;
+            reinterpret_cast<float4*>(wts + s * C)[lane] = make_float4(ex2(w[0]), ex2(w[1]), ex2(w[2]), ex2(w[3]));
+            if (lane == 0) gam[g % Cfg::kGam] = ex2(all);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
+            return true;
+        });
+    } else if (warp >= 4 && warp < 8) {
+        walk([&](const GatedUnit&, bool, int, int nv, int64_t g) {
+            const int s = static_cast<int>(g % Cfg::NS);
+            const uint32_t ph = (g / Cfg::NS) & 1;
+            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], ph, abort_flag, tmo, 0x630 + s)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_FULL + s], ph, abort_flag, tmo, 0x638 + s)) return false;
+            const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE, lo = y + Cfg::TILE;
+            const float* w = wts + s * C;
+            // warp w takes rows 32 (w - 4) ..; its lanes four rows of eight 16-byte pieces at a time
+            const int r0 = (warp - 4) * 32 + (lane >> 3);
+#pragma unroll 2
+            for (int it = 0; it < 8; ++it) {
+                const int row = r0 + 4 * it;
+                const float f = w[row];
+#pragma unroll
+                for (int pn = 0; pn < Cfg::NPAN; ++pn) {
+                    const uint32_t at = pn * kPanel + row * 128 + (lane & 7) * 16;
+                    uint32_t a[4], hi[4], l[4];
+                    ld_shared_v4(x + at, a[0], a[1], a[2], a[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float u0 = f * bf16_lo(a[e]), u1 = f * bf16_hi(a[e]);
+                        hi[e] = pack_bf16x2(u0, u1);
+                        l[e] = pack_bf16x2(u0 - bf16_lo(hi[e]), u1 - bf16_hi(hi[e]));
+                        if (row >= nv) hi[e] = l[e] = 0u;
+                    }
+                    st_shared_v4(x + at, hi[0], hi[1], hi[2], hi[3]);
+                    st_shared_v4(lo + at, l[0], l[1], l[2], l[3]);
+                    if (row >= nv) st_shared_v4(y + at, 0u, 0u, 0u, 0u);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[Cfg::B_SCALED + s]);
+            return true;
+        });
+    } else if (warp >= 8 && warp < 8 + 4 * Cfg::NPAN) {
+        const int sub = warp & 3, half = (warp - 8) >> 2;
+        const int row = D == 128 ? sub * 32 + lane : (lane < 16 ? sub * 16 + lane : -1);
+        const uint32_t lane_off = (static_cast<uint32_t>(sub * 32) << 16) + half * 64;
+        uint8_t* panel = smem + Cfg::OFF_SB + half * Cfg::SB_PANEL;
+        constexpr int kRows = D / 4;  // rows of this warp
+        float S[64];
+        int64_t g = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+            const bool rev = i >= p.n_units;
+            const int64_t u = rev ? i - p.n_units : i;
+            const GatedUnit un = gated_unit(p, u);
+            const int nch = (un.len + C - 1) / C;
+            if (nch == 0) continue;
+            const float* in = rev ? p.dstate : (p.state ? p.state : p.s0);
+            float* out = rev ? p.dstate : p.state;
+            const int64_t at = u * D * D + static_cast<int64_t>(row < 0 ? 0 : row) * D + half * 64;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float4 f = in && row >= 0 ? reinterpret_cast<const float4*>(in + at)[j] : make_float4(0, 0, 0, 0);
+                S[4 * j] = f.x;
+                S[4 * j + 1] = f.y;
+                S[4 * j + 2] = f.z;
+                S[4 * j + 3] = f.w;
+            }
+            uint8_t* slots = static_cast<uint8_t*>(rev ? p.e_states : p.s_states) + un.slot0 * Cfg::SB;
+            for (int cc = 0; cc < nch; ++cc, ++g) {
+                const int c = rev ? nch - 1 - cc : cc;
+                const int b = static_cast<int>(g & 1);
+                // the state before this chunk, as bf16, to its slot
+                if (lane == 0) bulk_wait_group_read<0>();
+                __syncwarp();
+                if (row >= 0) {
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch)
+                        st_shared_v4(smem_u32(panel) + sw128_off(row, ch), pack_bf16x2(S[8 * ch], S[8 * ch + 1]),
+                                     pack_bf16x2(S[8 * ch + 2], S[8 * ch + 3]),
+                                     pack_bf16x2(S[8 * ch + 4], S[8 * ch + 5]),
+                                     pack_bf16x2(S[8 * ch + 6], S[8 * ch + 7]));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    const int off = half * Cfg::SB_PANEL + sub * kRows * 128;
+                    bulk_store(slots + static_cast<int64_t>(c) * Cfg::SB + off, smem + Cfg::OFF_SB + off, kRows * 128);
+                    bulk_commit_group();
+                }
+                if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x640 + b)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float gamma = gam[g % Cfg::kGam];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    ld32f(tmem + lane_off + b * D + h * 32, x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) S[h * 32 + j] = fmaf(gamma, S[h * 32 + j], x[j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[Cfg::B_UEMPTY + b]);
+            }
+            if (ok && out && row >= 0) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    reinterpret_cast<float4*>(out + at)[j] =
+                        make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+            }
+        }
+        if (lane == 0) bulk_wait_group<0>();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Cfg::TM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Output of the chunks.  Per chunk
+//     A = Q K^T,  P_ij = e^{G_i - G_j} A_ij (j <= i),  O = e^{G_i} (Q S) + P V.
+// The decay of a whole 32 x 32 block left of the diagonal is the product of a
+// column's factor, e^{R - G_j} with R the prefix at the block's end, and a
+// row's, e^{G_i - R}; only the diagonal blocks take an exponential per element.
+//   warp 0       TMA producer        warp 1  MMA issuer
+//   warp 2       decays; zeroes the rows behind a sequence's end in V
+//   warps 4-7    scores -> P (bf16, over the scores in tensor memory)
+//   warps 8-15   (8-11 at D = 64) O -> bf16, staged in the chunk's Q tile -> TMA store
+// ---------------------------------------------------------------------------
+template <int D>
+struct OutCfg {
+    static constexpr int kThreads = 512;
+    static constexpr int NPAN = D / 64;
+    static constexpr int TILE = C * D * 2;
+    static constexpr int STAGE = 3 * TILE;
+    static constexpr int NS = D == 128 ? 2 : 4;
+    static constexpr int SB = D * D * 2, SB_PANEL = D * 128;
+    static constexpr int OFF_SB = NS * STAGE;
+    static constexpr int OFF_G = OFF_SB + SB;  // [NS]: 128 prefix sums, 96 column factors (the last block needs none)
+    static constexpr int G_BYTES = (C + 96) * 4;
+    static constexpr int OFF_BAR = OFF_G + NS * G_BYTES;
+    static constexpr int B_FULL = 0, B_EMPTY = NS, B_GFULL = 2 * NS, B_SFULL = 3 * NS, B_SEMPTY = 3 * NS + 1,
+                         B_AFULL = 3 * NS + 2, B_PFULL = 3 * NS + 4, B_OFULL = 3 * NS + 6, B_OEMPTY = 3 * NS + 7,
+                         B_DONE = 3 * NS + 8, NBAR = 3 * NS + 9;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int TM_A = 0, TM_O1 = 256, TM_O2 = 256 + D;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(512, 1)
+    gated_out_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_slots) {
+    using Cfg = OutCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t tmo = p.timeout_ns;
+    const uint32_t sbase = smem_u32(smem);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::NS; ++s) {
+            mbar_init(&bar[Cfg::B_FULL + s], 1);
+            mbar_init(&bar[Cfg::B_EMPTY + s], 4 * Cfg::NPAN);
+            mbar_init(&bar[Cfg::B_GFULL + s], 1);
+        }
+        mbar_init(&bar[Cfg::B_SFULL], 1);
+        mbar_init(&bar[Cfg::B_SEMPTY], 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bar[Cfg::B_AFULL + b], 1);
+            mbar_init(&bar[Cfg::B_PFULL + b], 4);
+        }
+        mbar_init(&bar[Cfg::B_OFULL], 1);
+        mbar_init(&bar[Cfg::B_OEMPTY], 4 * Cfg::NPAN);
+        mbar_init(&bar[Cfg::B_DONE], 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    auto walk = [&](auto&& f) -> bool {
+        int64_t g = 0;
+        for (int64_t i = blockIdx.x; i < n_slots; i += gridDim.x) {
+            const GatedChunk ch = gated_chunk(p, i, C);
+            if (ch.nv <= 0) continue;
+            if (!f(ch, i, g)) return false;
+            ++g;
+        }
+        return true;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int64_t started = 0;
+            const bool ok = walk([&](const GatedChunk& ch, int64_t slot, int64_t g) {
+                const int s = static_cast<int>(g % Cfg::NS);
+                if (g >= Cfg::NS &&
+                    !mbar_wait(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x700 + s))
+                    return false;
+                mbar_arrive_expect_tx(&bar[Cfg::B_FULL + s], 3 * Cfg::TILE);
+                uint8_t* st = smem + s * Cfg::STAGE;
+#pragma unroll
+                for (int pn = 0; pn < Cfg::NPAN; ++pn) {
+                    tma_load_3d(st + pn * kPanel, &m.q, &bar[Cfg::B_FULL + s], pn * 64, ch.row, ch.group);
+                    tma_load_3d(st + Cfg::TILE + pn * kPanel, &m.k, &bar[Cfg::B_FULL + s], pn * 64, ch.row, ch.group);
+                    tma_load_3d(st + 2 * Cfg::TILE + pn * kPanel, &m.v, &bar[Cfg::B_FULL + s], pn * 64, ch.row,
+                                ch.group);
+                }
+                started = g + 1;
+                if (g >= 1 && !mbar_wait(&bar[Cfg::B_SEMPTY], (g + 1) & 1, abort_flag, tmo, 0x708)) return false;
+                mbar_arrive_expect_tx(&bar[Cfg::B_SFULL], Cfg::SB);
+                bulk_load(smem + Cfg::OFF_SB, static_cast<const uint8_t*>(p.s_states) + slot * Cfg::SB, Cfg::SB,
+                          &bar[Cfg::B_SFULL]);
+                return true;
+            });
+            if (!ok || *abort_flag) {
+                for (int64_t g = started > Cfg::NS ? started - Cfg::NS : 0; g < started; ++g)
+                    mbar_wait_drain(&bar[Cfg::B_FULL + g % Cfg::NS], (g / Cfg::NS) & 1, tmo);
+                // the last state copy was started for chunk started - 1, or, if its slot was not free, started - 2
+                if (started >= 2) mbar_wait_drain(&bar[Cfg::B_SFULL], (started - 2) & 1, tmo);
+                if (ok && started >= 1) mbar_wait_drain(&bar[Cfg::B_SFULL], (started - 1) & 1, tmo);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t kIdA = idesc_bf16_f32(C, C, false, false);
+            constexpr uint32_t kIdO = idesc_bf16_f32(C, D, false, true);
+            bool issued = false;
+            auto scores = [&](int64_t g) -> bool {
+                const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
+                if (!mbar_wait(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x710 + s)) return false;
+                // the buffer's last P was read by the product of chunk g - 2, which O of that chunk waited for
+                if (g >= 2 && !mbar_wait(&bar[Cfg::B_OFULL], (g - 2) & 1, abort_flag, tmo, 0x718)) return false;
+                tc_fence_after();
+                const uint32_t q = sbase + s * Cfg::STAGE, k = q + Cfg::TILE;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16_ss(tmem + Cfg::TM_A + b * C, sdesc_sw128(tile_k(q, ks, kPanel), 16, 1024),
+                                sdesc_sw128(tile_k(k, ks, kPanel), 16, 1024), kIdA, ks > 0);
+                mma_commit(&bar[Cfg::B_AFULL + b]);
+                issued = true;
+                return true;
+            };
+            auto output = [&](int64_t g) -> bool {
+                const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
+                if (g >= 1 && !mbar_wait(&bar[Cfg::B_OEMPTY], (g + 1) & 1, abort_flag, tmo, 0x720)) return false;
+                if (!mbar_wait(&bar[Cfg::B_SFULL], g & 1, abort_flag, tmo, 0x728)) return false;
+                tc_fence_after();
+                const uint32_t q = sbase + s * Cfg::STAGE, v = q + 2 * Cfg::TILE, sb = sbase + Cfg::OFF_SB;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16_ss(tmem + Cfg::TM_O1, sdesc_sw128(tile_k(q, ks, kPanel), 16, 1024),
+                                sdesc_sw128(sb + ks * 2048, Cfg::SB_PANEL, 1024), kIdO, ks > 0);
+                mma_commit(&bar[Cfg::B_SEMPTY]);
+                if (!mbar_wait(&bar[Cfg::B_PFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x730 + b)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+                    mma_bf16_ts(tmem + Cfg::TM_O2, tmem + Cfg::TM_A + b * C + ks * 8,
+                                sdesc_sw128(v + ks * 2048, kPanel, 1024), kIdO, ks > 0);
+                mma_commit(&bar[Cfg::B_OFULL]);
+                return true;
+            };
+            // the scores run one chunk ahead of the output
+            int64_t last = -1;
+            bool ok = walk([&](const GatedChunk&, int64_t, int64_t g) {
+                if (!scores(g)) return false;
+                if (g >= 1 && !output(g - 1)) return false;
+                last = g;
+                return true;
+            });
+            if (ok && last >= 0) output(last);
+            if (issued) {
+                mma_commit(&bar[Cfg::B_DONE]);
+                mbar_wait_drain(&bar[Cfg::B_DONE], 0, tmo);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        walk([&](const GatedChunk& ch, int64_t, int64_t g) {
+            const int s = static_cast<int>(g % Cfg::NS);
+            float x[4], G[4];
+            load_gates(p, ch.row0, ch.nv, x);
+            scan_up(x, G);
+            const float R = __shfl_sync(0xffffffffu, G[3], lane | 7);  // prefix at the end of the 32-token block
+            // tiles landed: the slot's last readers are done
+            if (!mbar_wait_warp(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x740 + s)) return false;
+            float4* o = reinterpret_cast<float4*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES);
+            o[lane] = make_float4(G[0], G[1], G[2], G[3]);
+            if (lane < 24) o[32 + lane] = make_float4(ex2(R - G[0]), ex2(R - G[1]), ex2(R - G[2]), ex2(R - G[3]));
+            if (ch.nv < C) {
+                zero_rows<D>(sbase + s * Cfg::STAGE + 2 * Cfg::TILE, ch.nv);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
+            return true;
+        });
+    } else if (warp >= 4 && warp < 8) {
+        const int sub = warp & 3, row = sub * 32 + lane;
+        walk([&](const GatedChunk&, int64_t, int64_t g) {
+            const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
+            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x750 + s)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_AFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x758 + b)) return false;
+            tc_fence_after();
+            const float* G = reinterpret_cast<const float*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES);
+            const float* F = G + C;
+            const uint32_t tm = tmem + Cfg::TM_A + b * C + (static_cast<uint32_t>(sub * 32) << 16);
+            const float Gi = G[row];
+            // half h of the keys: scores in columns 64 h .., P written to columns 32 h .. (already read)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int jb = 2 * h + q;  // block of 32 keys; warp-uniform cases
+                    if (jb > sub) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[16 * q + e] = 0u;
+                        continue;
+                    }
+                    float a[32];
+                    ld32f(tm + jb * 32, a);
+                    if (jb < sub) {
+                        const float f = ex2(Gi - G[jb * 32 + 31]);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 c = reinterpret_cast<const float4*>(F + jb * 32)[e];
+                            w[16 * q + 2 * e] = pack_bf16x2(a[4 * e] * (f * c.x), a[4 * e + 1] * (f * c.y));
+                            w[16 * q + 2 * e + 1] = pack_bf16x2(a[4 * e + 2] * (f * c.z), a[4 * e + 3] * (f * c.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 c = reinterpret_cast<const float4*>(G + jb * 32)[e];
+                            const float d[4] = {c.x, c.y, c.z, c.w};
+                            float y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] = 4 * e + k <= lane ? a[4 * e + k] * ex2(Gi - d[k]) : 0.f;
+                            w[16 * q + 2 * e] = pack_bf16x2(y[0], y[1]);
+                            w[16 * q + 2 * e + 1] = pack_bf16x2(y[2], y[3]);
+                        }
+                    }
+                }
+                tmem_st32(tm + h * 32, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[Cfg::B_PFULL + b]);
+            return true;
+        });
+    } else if (warp >= 8 && warp < 8 + 4 * Cfg::NPAN) {
+        const int sub = warp & 3, half = (warp - 8) >> 2, row = sub * 32 + lane;
+        const uint32_t lane_off = (static_cast<uint32_t>(sub * 32) << 16) + half * 64;
+        walk([&](const GatedChunk& ch, int64_t, int64_t g) {
+            const int s = static_cast<int>(g % Cfg::NS);
+            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x760 + s)) return false;
+            const float f = ex2(reinterpret_cast<const float*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES)[row]);
+            if (!mbar_wait_warp(&bar[Cfg::B_OFULL], g & 1, abort_flag, tmo, 0x768)) return false;
+            tc_fence_after();
+            const uint32_t panel = sbase + s * Cfg::STAGE + half * kPanel;  // Q, read by both of its products
+            uint16_t* out = static_cast<uint16_t*>(p.o) + (ch.row0 + row) * D + half * 64;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[32], y[32];
+                ld32f(tmem + Cfg::TM_O1 + lane_off + h * 32, x);
+                ld32f(tmem + Cfg::TM_O2 + lane_off + h * 32, y);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = fmaf(f, x[e], y[e]);
+                if (ch.nv == C) {
+                    put_row32(panel, row, 4 * h, x);
+                } else if (row < ch.nv) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<uint4*>(out + h * 32)[e] =
+                            make_uint4(pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
+                                       pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
+                }
+            }
+            tc_fence_before();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar[Cfg::B_OEMPTY]);
+                if (ch.nv == C) {
+                    tma_store_3d(&m.o, smem + s * Cfg::STAGE + half * kPanel + sub * 32 * 128, half * 64,
+                                 ch.row + sub * 32, ch.group);
+                    bulk_commit_group();
+                    bulk_wait_group_read<0>();
+                }
+                mbar_arrive(&bar[Cfg::B_EMPTY + s]);
+            }
+            return true;
+        });
+        if (lane == 0) bulk_wait_group<0>();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the chunks.  With j the lane (row) of an accumulator, per chunk
+//     T0 = K Q^T, T1 = V dO^T            -> P^T, W^T (decayed, i >= j; bf16 over T0)
+//     T2 = e^{G_i} (dO S^T) + W K        -> dq
+//     T3 = e^{G_C - G_j} (V E^T) + W^T Q -> dk
+//     T1 = e^{G_C - G_j} (K E) + P^T dO  -> dv
+// Each decayed part is scaled in tensor memory before its second product is
+// accumulated onto it; on the way its dot product with q (k) gives the terms
+// of dg that pass a chunk's edge.  The terms within the chunk are row and
+// column sums of M = w (q k)(do v) in fp32: what gate t gets is
+// sum_{i >= t} (row_i - column_i), whose terms cancel exactly but for fp32.
+//   warp 0       producer            warp 1  MMA issuer
+//   warp 2       decays; zeroes the rows behind a sequence's end
+//   warp 3       dg
+//   warps 4-11   everything else: two warps share 32 rows, each takes half of
+//                the columns
+// Tiles are loaded once each (one stage at D = 128: 192 KB), reloaded for the
+// next chunk as each dies, and dq, dk, dv are staged for their stores in the
+// dead tiles of K, Q and dO.
+// ---------------------------------------------------------------------------
+template <int D>
+struct GrCfg {
+    static constexpr int kThreads = 384;
+    static constexpr int NPAN = D / 64;
+    static constexpr int TILE = C * D * 2;
+    static constexpr int SB = D * D * 2, SB_PANEL = D * 128;
+    static constexpr int NS = D == 128 ? 1 : 2;
+    static constexpr int STAGE = 4 * TILE + 2 * SB;
+    // tiles of a stage
+    static constexpr int Q = 0, K = TILE, V = 2 * TILE, O = 3 * TILE, S = 4 * TILE, E = 4 * TILE + SB;
+    static constexpr int W_BYTES = C * C * 2;
+    // W^T: over S at D = 128 (S is dead by then), a tile of its own at D = 64
+    static constexpr int OFF_W = D == 128 ? S : NS * STAGE;
+    static constexpr int OFF_G = NS * STAGE + (D == 128 ? 0 : W_BYTES);
+    // [2][4][128]: prefix sums; e^{G_i}; e^{G_C - G_j}; e^{G_i - R}, R the prefix before i's block
+    static constexpr int OFF_ROWS = OFF_G + 2 * 4 * C * 4;  // sum_j M by block of 32 keys [4][128]
+    static constexpr int OFF_COLS = OFF_ROWS + 4 * C * 4;   // sum_i M by half [2][128]
+    static constexpr int OFF_RI = OFF_COLS + 2 * C * 4;     // e^{G_i} q_i . S do_i by half [2][128]
+    static constexpr int OFF_CJ = OFF_RI + 2 * C * 4;       // e^{G_C - G_j} k_j . E v_j by half [2][128]
+    static constexpr int OFF_ES = OFF_CJ + 2 * C * 4;       // e^{G_C} <E, S> by warp [8]
+    static constexpr int OFF_BAR = OFF_ES + 32;
+    // per stage: loads and releases of Q, K, V, dO, S, E
+    static constexpr int F_Q = 0, F_K = 1, F_V = 2, F_O = 3, F_S = 4, F_E = 5;
+    static constexpr int B_FULL = 0, B_EMPTY = 6 * NS, B_GFULL = 12 * NS, B_ABFULL = 12 * NS + NS, B_X = B_ABFULL + 1,
+                         B_Y = B_ABFULL + 2, B_Z = B_ABFULL + 3, B_P = B_ABFULL + 4, B_XYS = B_ABFULL + 5,
+                         B_ZS = B_ABFULL + 6, B_DQ = B_ABFULL + 7, B_DK = B_ABFULL + 8, B_DV = B_ABFULL + 9,
+                         B_FREE = B_ABFULL + 10 /* T2, T3, T1 read out */, B_SUMS = B_ABFULL + 13,
+                         B_SUMFREE = B_ABFULL + 14, B_DONE = B_ABFULL + 15, B_READ = B_ABFULL + 16,
+                         B_PAIR = B_ABFULL + 17 /* [4] */, NBAR = B_ABFULL + 21;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int T0 = 0, T1 = 128, T2 = 256, T3 = 384;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+// v[c] of lane l, summed over the lanes: lane c gets the sum of v[c].
+__device__ __forceinline__ float column_sums(float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int k = 0; k < s; ++k) {
+            const float keep = up ? v[k + s] : v[k], send = up ? v[k] : v[k + s];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        }
+    }
+    return v[0];
+}
+
+// Scale 32 accumulator columns in place by f and return their dot product with
+// the row's 32 bf16 values in four chunks of a swizzled panel row.
+__device__ __forceinline__ float scale_dot32(uint32_t taddr, float f, uint32_t panel, int row, int chunk0) {
+    float x[32];
+    ld32f(taddr, x);
+    uint32_t w[32];
+    float dot = 0.f;
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+        uint32_t a[4];
+        ld_shared_v4(panel + sw128_off(row, chunk0 + ch), a[0], a[1], a[2], a[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = 8 * ch + 2 * e;
+            x[i] *= f;
+            x[i + 1] *= f;
+            dot = fmaf(x[i], bf16_lo(a[e]), dot);
+            dot = fmaf(x[i + 1], bf16_hi(a[e]), dot);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(x[i]);
+    tmem_st32(taddr, w);
+    return dot;
+}
+
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    gated_grad_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_slots) {
+    using Cfg = GrCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t tmo = p.timeout_ns;
+    const uint32_t sbase = smem_u32(smem);
+    // releases of K, Q and dO come from the warps that store dq, dk and dv out of them
+    constexpr int kStorers = Cfg::NPAN == 2 ? 8 : 4;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::NS; ++s) {
+            for (int t = 0; t < 6; ++t) {
+                mbar_init(&bar[Cfg::B_FULL + 6 * s + t], 1);
+                mbar_init(&bar[Cfg::B_EMPTY + 6 * s + t], t == Cfg::F_Q || t == Cfg::F_K || t == Cfg::F_O ? kStorers : 1);
+            }
+            mbar_init(&bar[Cfg::B_GFULL + s], 1);
+        }
+        for (int b : {Cfg::B_ABFULL, Cfg::B_X, Cfg::B_Y, Cfg::B_Z, Cfg::B_DQ, Cfg::B_DK, Cfg::B_DV, Cfg::B_SUMFREE,
+                      Cfg::B_DONE})
+            mbar_init(&bar[b], 1);
+        for (int b : {Cfg::B_P, Cfg::B_XYS, Cfg::B_ZS, Cfg::B_FREE, Cfg::B_FREE + 1, Cfg::B_FREE + 2, Cfg::B_SUMS, Cfg::B_READ})
+            mbar_init(&bar[b], 8);
+        for (int b = 0; b < 4; ++b) mbar_init(&bar[Cfg::B_PAIR + b], 2);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    auto walk = [&](auto&& f) -> bool {
+        int64_t g = 0;
+        for (int64_t i = blockIdx.x; i < n_slots; i += gridDim.x) {
+            const GatedChunk ch = gated_chunk(p, i, C);
+            if (ch.nv <= 0) continue;
+            if (!f(ch, i, g)) return false;
+            ++g;
+        }
+        return true;
+    };
+    auto full = [&](int s, int t) { return &bar[Cfg::B_FULL + 6 * s + t]; };
+    auto empty = [&](int s, int t) { return &bar[Cfg::B_EMPTY + 6 * s + t]; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int64_t started[6] = {0, 0, 0, 0, 0, 0};
+            const bool ok = walk([&](const GatedChunk& ch, int64_t slot, int64_t g) {
+                const int s = static_cast<int>(g % Cfg::NS);
+                uint8_t* st = smem + s * Cfg::STAGE;
+                // in the order in which the tiles of the chunk before die
+                constexpr int order[6] = {Cfg::F_V, Cfg::F_E, Cfg::F_S, Cfg::F_K, Cfg::F_Q, Cfg::F_O};
+#pragma unroll
+                for (int k = 0; k < 6; ++k) {
+                    const int t = order[k];
+                    if (g >= Cfg::NS && !mbar_wait(empty(s, t), ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x800 + t))
+                        return false;
+                    if (t == Cfg::F_S || t == Cfg::F_E) {
+                        mbar_arrive_expect_tx(full(s, t), Cfg::SB);
+                        bulk_load(st + (t == Cfg::F_S ? Cfg::S : Cfg::E),
+                                  static_cast<const uint8_t*>(t == Cfg::F_S ? p.s_states : p.e_states) + slot * Cfg::SB,
+                                  Cfg::SB, full(s, t));
+                    } else {
+                        const CUtensorMap* map =
+                            t == Cfg::F_Q ? &m.q : (t == Cfg::F_K ? &m.k : (t == Cfg::F_V ? &m.v : &m.d_o));
+                        mbar_arrive_expect_tx(full(s, t), Cfg::TILE);
+#pragma unroll
+                        for (int pn = 0; pn < Cfg::NPAN; ++pn)
+                            tma_load_3d(st + t * Cfg::TILE + pn * kPanel, map, full(s, t), pn * 64, ch.row, ch.group);
+                    }
+                    started[t] = g + 1;
+                }
+                // the next chunk's tiles into L2 while this one is computed
+                const int64_t next = slot + gridDim.x;
+                if (next < n_slots) {
+                    const GatedChunk c2 = gated_chunk(p, next, C);
+                    if (c2.nv > 0) {
+#pragma unroll
+                        for (int pn = 0; pn < Cfg::NPAN; ++pn) {
+                            tma_prefetch_l2_3d(&m.q, pn * 64, c2.row, c2.group);
+                            tma_prefetch_l2_3d(&m.k, pn * 64, c2.row, c2.group);
+                            tma_prefetch_l2_3d(&m.v, pn * 64, c2.row, c2.group);
+                            tma_prefetch_l2_3d(&m.d_o, pn * 64, c2.row, c2.group);
+                        }
+                        bulk_prefetch_l2(static_cast<const uint8_t*>(p.s_states) + next * Cfg::SB, Cfg::SB);
+                        bulk_prefetch_l2(static_cast<const uint8_t*>(p.e_states) + next * Cfg::SB, Cfg::SB);
+                    }
+                }
+                return true;
+            });
+            if (!ok || *abort_flag)
+                for (int t = 0; t < 6; ++t)
+                    for (int64_t g = started[t] > Cfg::NS ? started[t] - Cfg::NS : 0; g < started[t]; ++g)
+                        mbar_wait_drain(full(static_cast<int>(g % Cfg::NS), t), (g / Cfg::NS) & 1, tmo);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t kIdT = idesc_bf16_f32(C, C, false, false);   // scores: both operands K-major
+            constexpr uint32_t kIdS = idesc_bf16_f32(C, D, false, false);   // .. S^T, .. E^T
+            constexpr uint32_t kIdB = idesc_bf16_f32(C, D, false, true);    // .. E, P^T dO, W^T Q
+            constexpr uint32_t kIdW = idesc_bf16_f32(C, D, true, true);     // W K, W held transposed
+            bool issued = false;
+            auto wait = [&](int b, int64_t phase, unsigned where) {
+                return mbar_wait(&bar[b], static_cast<uint32_t>(phase & 1), abort_flag, tmo, where);
+            };
+            walk([&](const GatedChunk&, int64_t, int64_t g) {
+                const int s = static_cast<int>(g % Cfg::NS);
+                const int64_t k = g / Cfg::NS;
+                const uint32_t st = sbase + s * Cfg::STAGE;
+                const uint32_t q = st + Cfg::Q, kk = st + Cfg::K, v = st + Cfg::V, o = st + Cfg::O, sb = st + Cfg::S,
+                               eb = st + Cfg::E, wt = sbase + Cfg::OFF_W;
+                auto loaded = [&](int t) { return wait(Cfg::B_FULL + 6 * s + t, k, 0x810 + t); };
+                // T0, T1: scores (T0 and T1 of the chunk before are consumed and read)
+                if (!loaded(Cfg::F_Q) || !loaded(Cfg::F_K)) return false;
+                if (g >= 1 && (!wait(Cfg::B_DV, g - 1, 0x818) || !wait(Cfg::B_FREE + 2, g - 1, 0x819))) return false;
+                tc_fence_after();
+                issued = true;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16_ss(tmem + Cfg::T0, sdesc_sw128(tile_k(kk, ks, kPanel), 16, 1024),
+                                sdesc_sw128(tile_k(q, ks, kPanel), 16, 1024), kIdT, ks > 0);
+                if (!loaded(Cfg::F_V) || !loaded(Cfg::F_O)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16_ss(tmem + Cfg::T1, sdesc_sw128(tile_k(v, ks, kPanel), 16, 1024),
+                                sdesc_sw128(tile_k(o, ks, kPanel), 16, 1024), kIdT, ks > 0);
+                mma_commit(&bar[Cfg::B_ABFULL]);
+                // T2 = dO S^T
+                if (!loaded(Cfg::F_S)) return false;
+                if (g >= 1 && !wait(Cfg::B_FREE + 0, g - 1, 0x81a)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16_ss(tmem + Cfg::T2, sdesc_sw128(tile_k(o, ks, kPanel), 16, 1024),
+                                sdesc_sw128(tile_k(sb, ks, Cfg::SB_PANEL), 16, 1024), kIdS, ks > 0);
+                mma_commit(&bar[Cfg::B_X]);
+                // T3 = V E^T
+                if (!loaded(Cfg::F_E)) return false;
+                if (g >= 1 && !wait(Cfg::B_FREE + 1, g - 1, 0x81b)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16_ss(tmem + Cfg::T3, sdesc_sw128(tile_k(v, ks, kPanel), 16, 1024),
+                                sdesc_sw128(tile_k(eb, ks, Cfg::SB_PANEL), 16, 1024), kIdS, ks > 0);
+                mma_commit(&bar[Cfg::B_Y]);
+                mma_commit(empty(s, Cfg::F_V));
+                // T1 = K E once the scores there are read
+                if (!wait(Cfg::B_P, g, 0x81c)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16_ss(tmem + Cfg::T1, sdesc_sw128(tile_k(kk, ks, kPanel), 16, 1024),
+                                sdesc_sw128(eb + ks * 2048, Cfg::SB_PANEL, 1024), kIdB, ks > 0);
+                mma_commit(&bar[Cfg::B_Z]);
+                mma_commit(empty(s, Cfg::F_E));
+                // onto the scaled parts
+                if (!wait(Cfg::B_XYS, g, 0x81d)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+                    mma_bf16_ss(tmem + Cfg::T2, sdesc_sw128(wt + ks * 2048, kPanel, 1024),
+                                sdesc_sw128(kk + ks * 2048, kPanel, 1024), kIdW, 1);
+                mma_commit(&bar[Cfg::B_DQ]);
+                mma_commit(empty(s, Cfg::F_S));
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+                    mma_bf16_ts(tmem + Cfg::T3, tmem + Cfg::T0 + 64 + ks * 8,
+                                sdesc_sw128(q + ks * 2048, kPanel, 1024), kIdB, 1);
+                mma_commit(&bar[Cfg::B_DK]);
+                if (!wait(Cfg::B_ZS, g, 0x81e)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+                    mma_bf16_ts(tmem + Cfg::T1, tmem + Cfg::T0 + ks * 8, sdesc_sw128(o + ks * 2048, kPanel, 1024),
+                                kIdB, 1);
+                mma_commit(&bar[Cfg::B_DV]);
+                return true;
+            });
+            if (issued) {
+                mma_commit(&bar[Cfg::B_DONE]);
+                mbar_wait_drain(&bar[Cfg::B_DONE], 0, tmo);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        walk([&](const GatedChunk& ch, int64_t, int64_t g) {
+            const int s = static_cast<int>(g % Cfg::NS);
+            const uint32_t ph = (g / Cfg::NS) & 1;
+            float x[4], G[4], B[4], all;
+            load_gates(p, ch.row0, ch.nv, x);
+            scan_up(x, G);
+            scan_down(x, B, all);
+            float R = __shfl_sync(0xffffffffu, G[3], ((lane >> 3) * 8 + 31) & 31);  // prefix before the block
+            if (lane < 8) R = 0.f;
+            for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_O})
+                if (!mbar_wait_warp(full(s, t), ph, abort_flag, tmo, 0x820 + t)) return false;
+            // two sets of decays: the set's last readers, in chunk g - 2, were done before these tiles were loaded
+            float4* o = reinterpret_cast<float4*>(smem + Cfg::OFF_G + (g & 1) * 4 * C * 4);
+            o[lane] = make_float4(G[0], G[1], G[2], G[3]);
+            o[32 + lane] = make_float4(ex2(G[0]), ex2(G[1]), ex2(G[2]), ex2(G[3]));
+            o[64 + lane] = make_float4(ex2(B[0]), ex2(B[1]), ex2(B[2]), ex2(B[3]));
+            o[96 + lane] = make_float4(ex2(G[0] - R), ex2(G[1] - R), ex2(G[2] - R), ex2(G[3] - R));
+            if (ch.nv < C) {
+                for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_O}) zero_rows<D>(sbase + s * Cfg::STAGE + t * Cfg::TILE, ch.nv);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
+            return true;
+        });
+    } else if (warp == 3) {
+        walk([&](const GatedChunk& ch, int64_t, int64_t g) {
+            if (!mbar_wait_warp(&bar[Cfg::B_SUMS], g & 1, abort_flag, tmo, 0x830)) return false;
+            const float4* rows = reinterpret_cast<const float4*>(smem + Cfg::OFF_ROWS);
+            const float4* cols = reinterpret_cast<const float4*>(smem + Cfg::OFF_COLS);
+            const float4* ri = reinterpret_cast<const float4*>(smem + Cfg::OFF_RI);
+            const float4* cj = reinterpret_cast<const float4*>(smem + Cfg::OFF_CJ);
+            const float* es = reinterpret_cast<const float*>(smem + Cfg::OFF_ES);
+            auto get = [&](const float4* a, int n, float (&x)[4]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = 0.f;
+                for (int k = 0; k < n; ++k) {
+                    const float4 f = a[32 * k + lane];
+                    x[0] += f.x;
+                    x[1] += f.y;
+                    x[2] += f.z;
+                    x[3] += f.w;
+                }
+            };
+            float r[4], c[4], u[4], d[4];
+            get(rows, (lane >> 3) + 1, r);  // blocks of keys up to the reader's own
+            get(cols, 2, c);
+            get(ri, 2, u);
+            get(cj, 2, d);
+            float e0 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) e0 += es[k];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (4 * lane + e >= ch.nv) r[e] = c[e] = u[e] = d[e] = 0.f;
+                u[e] += r[e] - c[e];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[Cfg::B_SUMFREE]);
+            float after[4], all, upto[4];
+            scan_down(u, after, all);  // over i > t
+            scan_up(d, upto);          // over j <= t
+            if (p.dg != nullptr) {
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dg) + ch.row0 + 4 * lane;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * lane + e < ch.nv) out[e] = __float2bfloat16_rn(e0 + after[e] + u[e] + (upto[e] - d[e]));
+            }
+            return true;
+        });
+    } else {
+        const int sub = warp & 3, half = (warp - 4) >> 2, row = sub * 32 + lane;
+        constexpr int HC = D / 2;  // columns of this thread in the D-wide tiles
+        const uint32_t lanes = static_cast<uint32_t>(sub * 32) << 16;
+        const uint32_t dcol = lanes + half * HC;
+        const int pan = D == 128 ? half : 0, ch0 = D == 128 ? 0 : 4 * half;  // this thread's panel and first 16-byte piece
+        float* rows = reinterpret_cast<float*>(smem + Cfg::OFF_ROWS);
+        float* cols = reinterpret_cast<float*>(smem + Cfg::OFF_COLS);
+        float* ri = reinterpret_cast<float*>(smem + Cfg::OFF_RI);
+        float* cj = reinterpret_cast<float*>(smem + Cfg::OFF_CJ);
+        float* es = reinterpret_cast<float*>(smem + Cfg::OFF_ES);
+        walk([&](const GatedChunk& ch, int64_t, int64_t g) {
+            const int s = static_cast<int>(g % Cfg::NS);
+            const uint32_t ph = (g / Cfg::NS) & 1, gp = static_cast<uint32_t>(g & 1);
+            const uint32_t st = sbase + s * Cfg::STAGE;
+            auto wait = [&](int b, uint32_t parity, unsigned where) {
+                return mbar_wait_warp(&bar[b], parity, abort_flag, tmo, where);
+            };
+            auto arrive = [&](int b) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[b]);
+            };
+            if (!wait(Cfg::B_GFULL + s, ph, 0x840)) return false;
+            const float* G = reinterpret_cast<const float*>(smem + Cfg::OFF_G + gp * 4 * C * 4);
+            const float *Pre = G + C, *Suf = G + 2 * C, *F = G + 3 * C;
+            // the sums of the chunk before are read
+            if (g >= 1 && !wait(Cfg::B_SUMFREE, gp ^ 1u, 0x841)) return false;
+            // e^{G_C} <E, S>, a share of rows per thread
+            if (!wait(Cfg::B_FULL + 6 * s + Cfg::F_S, ph, 0x842) || !wait(Cfg::B_FULL + 6 * s + Cfg::F_E, ph, 0x843))
+                return false;
+            {
+                float acc = 0.f;
+                const int t = threadIdx.x - 128;
+#pragma unroll 2
+                for (int i = t * 16; i < Cfg::SB; i += 256 * 16) {
+                    uint32_t a[4], b[4];
+                    ld_shared_v4(st + Cfg::S + i, a[0], a[1], a[2], a[3]);
+                    ld_shared_v4(st + Cfg::E + i, b[0], b[1], b[2], b[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc = fmaf(bf16_lo(a[e]), bf16_lo(b[e]), acc);
+                        acc = fmaf(bf16_hi(a[e]), bf16_hi(b[e]), acc);
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                if (lane == 0) es[warp - 4] = Pre[C - 1] * acc;
+            }
+            // decayed scores of key row j = row, readers i in this half
+            if (!wait(Cfg::B_ABFULL, gp, 0x844)) return false;
+            tc_fence_after();
+            uint32_t pw[32], ww[32];
+            float csum = 0.f;
+            const float Gj = G[row];
+#pragma unroll
+            for (int qd = 0; qd < 2; ++qd) {
+                const int ib = 2 * half + qd;  // block of 32 readers; warp-uniform cases
+                if (ib < sub) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pw[16 * qd + e] = ww[16 * qd + e] = 0u;
+                    continue;
+                }
+                float a[32], b[32];
+                ld32f(tmem + Cfg::T0 + lanes + ib * 32, a);
+                ld32f(tmem + Cfg::T1 + lanes + ib * 32, b);
+                const float fj = ib > sub ? ex2(G[ib * 32 - 1] - Gj) : 0.f;
+                const bool rowin = row < ch.nv;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float w[2], pv[2], wv[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = ib * 32 + 2 * e + h;
+                        const bool in = rowin && i < ch.nv && i >= row;
+                        w[h] = ib > sub ? fj * F[i] : ex2(G[i] - Gj);
+                        pv[h] = in ? w[h] * a[2 * e + h] : 0.f;
+                        wv[h] = in ? w[h] * b[2 * e + h] : 0.f;
+                        a[2 * e + h] = in && i > row ? pv[h] * b[2 * e + h] : 0.f;  // M
+                        csum += a[2 * e + h];
+                    }
+                    pw[16 * qd + e] = pack_bf16x2(pv[0], pv[1]);
+                    ww[16 * qd + e] = pack_bf16x2(wv[0], wv[1]);
+                }
+                const float rs = column_sums(a);
+                rows[sub * C + ib * 32 + lane] = rs;
+            }
+            cols[half * C + row] = csum;
+            // every thread has read T0, T1 and S, whose place the results take
+            tc_fence_before();
+            arrive(Cfg::B_READ);
+            if (!wait(Cfg::B_X, gp, 0x845) || !wait(Cfg::B_READ, gp, 0x848)) return false;
+            tc_fence_after();
+            tmem_st32(tmem + Cfg::T0 + lanes + half * 32, pw);
+            tmem_st32(tmem + Cfg::T0 + lanes + 64 + half * 32, ww);
+            {
+                const uint32_t panel = sbase + Cfg::OFF_W + half * kPanel;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    st_shared_v4(panel + sw128_off(row, c), ww[4 * c], ww[4 * c + 1], ww[4 * c + 2], ww[4 * c + 3]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            fence_proxy_async_smem();
+            arrive(Cfg::B_P);
+            // scale the parts through the states, with their terms of dg
+            tc_fence_after();
+            float dot = 0.f;
+#pragma unroll
+            for (int h = 0; h < HC / 32; ++h)
+                dot += scale_dot32(tmem + Cfg::T2 + dcol + h * 32, Pre[row], st + Cfg::Q + pan * kPanel, row, ch0 + 4 * h);
+            ri[half * C + row] = dot;
+            if (!wait(Cfg::B_Y, gp, 0x846)) return false;
+            tc_fence_after();
+            dot = 0.f;
+#pragma unroll
+            for (int h = 0; h < HC / 32; ++h)
+                dot += scale_dot32(tmem + Cfg::T3 + dcol + h * 32, Suf[row], st + Cfg::K + pan * kPanel, row, ch0 + 4 * h);
+            cj[half * C + row] = dot;
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(Cfg::B_XYS);
+            arrive(Cfg::B_SUMS);
+            if (!wait(Cfg::B_Z, gp, 0x847)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < HC / 32; ++h) {
+                float x[32];
+                ld32f(tmem + Cfg::T1 + dcol + h * 32, x);
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(x[e] * Suf[row]);
+                tmem_st32(tmem + Cfg::T1 + dcol + h * 32, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(Cfg::B_ZS);
+            // results
+            auto result = [&](int ready, int tm, int freed, int tile, const CUtensorMap* map, void* dst) -> bool {
+                if (!wait(ready, gp, 0x850 + tile)) return false;
+                tc_fence_after();
+                const uint32_t panel = st + tile * Cfg::TILE + pan * kPanel;
+                uint16_t* out = static_cast<uint16_t*>(dst) + (ch.row0 + row) * D + half * HC;
+#pragma unroll
+                for (int h = 0; h < HC / 32; ++h) {
+                    float x[32];
+                    ld32f(tmem + tm + dcol + h * 32, x);
+                    if (ch.nv == C) {
+                        put_row32(panel, row, ch0 + 4 * h, x);
+                    } else if (row < ch.nv) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4*>(out + h * 32)[e] = make_uint4(
+                                pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
+                                pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
+                    }
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                arrive(Cfg::B_FREE + freed);
+                if (D == 64) {  // two warps fill a panel's 32 rows (three results a chunk)
+                    arrive(Cfg::B_PAIR + sub);
+                    if (!wait(Cfg::B_PAIR + sub, static_cast<uint32_t>((3 * g + freed) & 1), 0x849)) return false;
+                }
+                if (lane == 0 && (D == 128 || half == 0)) {
+                    if (ch.nv == C) {
+                        tma_store_3d(map, smem + s * Cfg::STAGE + tile * Cfg::TILE + pan * kPanel + sub * 32 * 128,
+                                     pan * 64, ch.row + sub * 32, ch.group);
+                        bulk_commit_group();
+                        bulk_wait_group_read<0>();
+                    }
+                    mbar_arrive(empty(s, tile));
+                }
+                __syncwarp();
+                return true;
+            };
+            return result(Cfg::B_DQ, Cfg::T2, 0, Cfg::F_K, &m.dq, p.dq) &&
+                   result(Cfg::B_DK, Cfg::T3, 1, Cfg::F_Q, &m.dk, p.dk_) &&
+                   result(Cfg::B_DV, Cfg::T1, 2, Cfg::F_O, &m.dv, p.dv_);
+        });
+        if (lane == 0) bulk_wait_group<0>();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename F>
+cudaError_t raise_smem(PerDeviceOnce& once, F kern, int bytes) {
+    return once.run([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+}
+unsigned grid_for(int64_t items, int num_sms) { return static_cast<unsigned>(items < num_sms ? items : num_sms); }
+
+template <int D>
+cudaError_t states_d(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s) {
+    static PerDeviceOnce once;
+    cudaError_t e = raise_smem(once, gated_states_tc_kernel<D>, StCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t items = grad ? 2 * p.n_units : p.n_units;
+    gated_states_tc_kernel<D><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items);
+    return cudaGetLastError();
+}
+template <int D>
+cudaError_t out_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+    static PerDeviceOnce once;
+    cudaError_t e = raise_smem(once, gated_out_tc_kernel<D>, OutCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t slots = p.groups * p.nc;
+    gated_out_tc_kernel<D><<<grid_for(slots, num_sms), OutCfg<D>::kThreads, OutCfg<D>::SMEM, s>>>(m, p, slots);
+    return cudaGetLastError();
+}
+template <int D>
+cudaError_t grad_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+    static PerDeviceOnce once;
+    cudaError_t e = raise_smem(once, gated_grad_tc_kernel<D>, GrCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t slots = p.groups * p.nc;
+    gated_grad_tc_kernel<D><<<grid_for(slots, num_sms), GrCfg<D>::kThreads, GrCfg<D>::SMEM, s>>>(m, p, slots);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s) {
+    return p.dk == 128 ? states_d<128>(p, m, grad, num_sms, s) : states_d<64>(p, m, grad, num_sms, s);
+}
+cudaError_t launch_gated_out_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+    return p.dk == 128 ? out_d<128>(p, m, num_sms, s) : out_d<64>(p, m, num_sms, s);
+}
+cudaError_t launch_gated_grad_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+    return p.dk == 128 ? grad_d<128>(p, m, num_sms, s) : grad_d<64>(p, m, num_sms, s);
+}
+
+}  // namespace la

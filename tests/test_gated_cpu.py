@@ -53,6 +53,10 @@ def test_reference_gate_zero_is_the_plain_recurrence():
 
 def test_kernel_choice(lib):
     assert la.la_gated_prefill_kernel(torch.bfloat16, 8, 128, 128) == "short"
+    assert la.la_gated_prefill_kernel(torch.bfloat16, 17, 128, 128) == "tc"
+    assert la.la_gated_prefill_kernel(torch.bfloat16, 17, 64, 64) == "tc"
+    assert la.la_gated_prefill_kernel(torch.bfloat16, 17, 128, 64) == "simt"
+    assert la.la_gated_prefill_kernel(torch.float32, 17, 128, 128) == "simt"
     assert la.la_gated_prefill_kernel(torch.float32, 777, 48, 80) == "simt"
     assert la.la_gated_prefill_kernel(torch.float32, 8, 48, 80) == "simt"
     assert la.la_gated_prefill_kernel(torch.bfloat16, 8, 129, 128) == "unsupported"
@@ -64,6 +68,8 @@ def test_workspace_sizes(lib):
     assert la.la_gated_prefill_backward_workspace_size(torch.float32, 2, 3, 65, 64, 32) == 2 * 2 * 3 * 3 * 64 * 32 * 4
     # packed: two chunks of 64 rows and one more for each of five sequences, after six offsets
     assert la.la_gated_prefill_workspace_size(torch.float32, 1, 3, 64, 64, 32, 5) == 256 + 3 * 7 * 64 * 32 * 4
+    # tensor cores: a bf16 state per chunk of 128
+    assert la.la_gated_prefill_workspace_size(torch.bfloat16, 2, 3, 129, 64, 64) == 2 * 2 * 3 * 64 * 64 * 2
     # the few-token kernel needs none, unless the longest packed sequence is not known
     assert la.la_gated_prefill_workspace_size(torch.bfloat16, 4, 4, 16, 128, 128) == 0
     assert la.la_gated_prefill_workspace_size(torch.bfloat16, 1, 4, 16, 128, 128, 2) > 0
@@ -108,6 +114,10 @@ def test_more_refusals(lib):
     inv, uns = la.LA_ERR_INVALID_ARG, la.LA_ERR_UNSUPPORTED
     assert _prefill(lib, o=None) == inv and _prefill(lib, state=None) == inv
     assert _prefill(lib, dtype=1, T=8, dk=64, dv=64, state=8) == uns      # few tokens, state not 16-byte aligned
+    for name in ("q", "k", "v", "o", "state"):                            # tensor cores: all of them
+        assert _prefill(lib, dtype=1, T=80, dk=64, dv=64, ws=256, wsb=1 << 20, **{name: 8}) == uns, name
+    for name in ("q", "k", "v", "s0", "do", "ds", "dq", "dk_", "dv_"):
+        assert _backward(lib, dtype=1, T=80, dk=64, dv=64, ws=256, wsb=1 << 20, **{name: 8}) == uns, name
     for name in ("do", "ds", "dq", "dk_", "dv_"):
         assert _backward(lib, **{name: None}) == inv
 
