@@ -240,45 +240,54 @@ def la_resolve_chunk(dtype: torch.dtype, dk: int, dv: int, chunk: int = 0) -> in
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "parts": 3}
 
 
-def _call(name: str, device: torch.device, stream, *args) -> None:
-    """Run one entry point with the tensors' device current, on its current
-    stream unless one is given."""
-    lib = load_library()
-    with torch.cuda.device(device):
-        _check(getattr(lib, name)(*args, _stream(torch.cuda.current_stream(device) if stream is None else stream)),
-               name)
-
-
-def _one_device(**tensors: Optional[torch.Tensor]) -> torch.device:
-    devs = {n: t.device for n, t in tensors.items() if t is not None}
-    first = next(iter(devs.values()))
-    for n, d in devs.items():
-        if d != first:
-            raise ValueError(f"{n} is on {d}, not on {first}")
-    return first
-
-
-def _expect(t: torch.Tensor, shape, name: str) -> None:
+def _arg(t: torch.Tensor, name: str, shape, dtype: torch.dtype, dev: int) -> int:
+    """The address of a contiguous tensor of this shape and type on CUDA device `dev`."""
+    # one test for the ordinary case: these calls cost as much as a small kernel
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    return _ptr(t, name, dtype)
 
 
-def _sequences(q, k, v, cu_seqlens, state, name: str):
-    """Shape checks that the sequence entry points share: (B, H, T, dk, dv, num_seqs)."""
+def _floats(t: torch.Tensor, name: str, numel: int, dev: int) -> int:
+    """The address of `numel` contiguous float32 values."""
+    if t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} floats (units * d_k * d_v), got {t.numel()}")
+    return _arg(t, name, t.shape, torch.float32, dev)
+
+
+def _device_of(q: torch.Tensor) -> int:
     if q.dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {q.dtype}")
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    return dev
+
+
+def _run(name: str, dev: int, stream, *args) -> None:
+    """Call one entry point with device `dev` current, on its current stream unless one is given."""
+    lib = _lib if _lib is not None else load_library()
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _run(name, dev, stream, *args)
+    status = getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status != LA_OK:
+        raise LinAttnError(status, name)
+
+
+def _sizes(q: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor], dev: int):
+    """(B, H, T, d_k, d_v, num_seqs, address of cu_seqlens) of the sequence entry points."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q must be [B, H, T, d_k] and v [B, H, T, d_v]")
     B, H, T, dk = q.shape
-    dv = v.shape[-1]
-    _expect(k, q.shape, "k")
-    _expect(v, (B, H, T, dv), "v")
-    num_seqs = _packed(cu_seqlens, B)
-    n_units = (num_seqs if cu_seqlens is not None else B) * H
-    if state.numel() != n_units * dk * dv:
-        raise ValueError(f"{name} must hold {n_units} x {dk} x {dv} floats "
-                         f"({'num_seqs' if cu_seqlens is not None else 'B'} * H units), got {state.numel()}")
-    return B, H, T, dk, dv, num_seqs
+    if cu_seqlens is None:
+        return B, H, T, dk, v.shape[3], 0, None
+    n = _packed(cu_seqlens, B)
+    return B, H, T, dk, v.shape[3], n, _arg(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
 
 
 def _packed(cu_seqlens: Optional[torch.Tensor], B: int) -> int:
@@ -293,10 +302,11 @@ def _packed(cu_seqlens: Optional[torch.Tensor], B: int) -> int:
     return cu_seqlens.numel() - 1
 
 
-def _workspace(workspace: Optional[torch.Tensor]):
+def _workspace(workspace: Optional[torch.Tensor], dev: int):
     if workspace is None:
         return None, 0
-    return _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    return (_arg(workspace, "workspace", workspace.shape, workspace.dtype, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def la_gated_prefill_workspace_size(dtype: torch.dtype, B: int, H: int, T: int, dk: int, dv: int,
@@ -320,16 +330,14 @@ def la_gated_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optio
                      max_seqlen: int = 0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Prefill of S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = q_t^T S_t.  q, k [B,H,T,d_k]; v, o [B,H,T,d_v];
     g [B,H,T] log gates (None: no decay); state as for la_prefill."""
-    B, H, T, dk, dv, num_seqs = _sequences(q, k, v, cu_seqlens, state, "state")
-    _expect(o, v.shape, "o")
-    if g is not None:
-        _expect(g, (B, H, T), "g")
-    dt = q.dtype
-    dev = _one_device(q=q, k=k, v=v, g=g, o=o, state=state, cu_seqlens=cu_seqlens, workspace=workspace)
-    ws, ws_bytes = _workspace(workspace)
-    _call("la_gated_prefill", dev, stream, _ptr(q, "q", dt), _ptr(k, "k", dt), _ptr(v, "v", dt), _ptr(g, "g", dt),
-          _ptr(o, "o", dt), _ptr(state, "state", torch.float32), _DTYPES[dt], B, H, T, dk, dv,
-          _ptr(cu_seqlens, "cu_seqlens"), num_seqs, int(max_seqlen), ws, ws_bytes)
+    dev, dt = _device_of(q), q.dtype
+    B, H, T, dk, dv, num_seqs, cu = _sizes(q, v, cu_seqlens, dev)
+    qs, vs = q.shape, (B, H, T, dv)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run("la_gated_prefill", dev, stream, _arg(q, "q", qs, dt, dev), _arg(k, "k", qs, dt, dev),
+         _arg(v, "v", vs, dt, dev), None if g is None else _arg(g, "g", (B, H, T), dt, dev),
+         _arg(o, "o", vs, dt, dev), _floats(state, "state", (num_seqs if cu_seqlens is not None else B) * H * dk * dv, dev),
+         _DTYPES[dt], B, H, T, dk, dv, cu, num_seqs, max_seqlen, ws, ws_bytes)
 
 
 def la_gated_prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor],
@@ -340,44 +348,32 @@ def la_gated_prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Gradient of la_gated_prefill.  state0: the incoming state (None: zero); dstate: gradient of the final state
     on entry, of the incoming one on return; dq, dk, dv, dg are written.  max_seqlen is not needed and taken only so
     that both directions can be called alike."""
-    B, H, T, d_k, d_v, num_seqs = _sequences(q, k, v, cu_seqlens, dstate, "dstate")
-    for name, t, like in (("do", do, v), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _expect(t, like.shape, name)
-    for name, t in (("g", g), ("dg", dg)):
-        if t is not None:
-            _expect(t, (B, H, T), name)
-    if state0 is not None and state0.numel() != dstate.numel():
-        raise ValueError("state0 must hold as many floats as dstate")
-    dt = q.dtype
-    dev = _one_device(q=q, k=k, v=v, g=g, state0=state0, do=do, dstate=dstate, dq=dq, dk=dk, dv=dv, dg=dg,
-                      cu_seqlens=cu_seqlens, workspace=workspace)
-    ws, ws_bytes = _workspace(workspace)
-    _call("la_gated_prefill_backward", dev, stream, _ptr(q, "q", dt), _ptr(k, "k", dt), _ptr(v, "v", dt),
-          _ptr(g, "g", dt), _ptr(state0, "state0", torch.float32), _ptr(do, "do", dt),
-          _ptr(dstate, "dstate", torch.float32), _ptr(dq, "dq", dt), _ptr(dk, "dk", dt), _ptr(dv, "dv", dt),
-          _ptr(dg, "dg", dt), _DTYPES[dt], B, H, T, d_k, d_v, _ptr(cu_seqlens, "cu_seqlens"), num_seqs, ws, ws_bytes)
+    dev, dt = _device_of(q), q.dtype
+    B, H, T, d_k, d_v, num_seqs, cu = _sizes(q, v, cu_seqlens, dev)
+    qs, vs, gs = q.shape, (B, H, T, d_v), (B, H, T)
+    floats = (num_seqs if cu_seqlens is not None else B) * H * d_k * d_v
+    ws, ws_bytes = _workspace(workspace, dev)
+    _run("la_gated_prefill_backward", dev, stream, _arg(q, "q", qs, dt, dev), _arg(k, "k", qs, dt, dev),
+         _arg(v, "v", vs, dt, dev), None if g is None else _arg(g, "g", gs, dt, dev),
+         None if state0 is None else _floats(state0, "state0", floats, dev), _arg(do, "do", vs, dt, dev),
+         _floats(dstate, "dstate", floats, dev), _arg(dq, "dq", qs, dt, dev), _arg(dk, "dk", qs, dt, dev),
+         _arg(dv, "dv", vs, dt, dev), None if dg is None else _arg(dg, "dg", gs, dt, dev), _DTYPES[dt], B, H, T,
+         d_k, d_v, cu, num_seqs, ws, ws_bytes)
 
 
 def la_gated_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor],
                          o: torch.Tensor, state: torch.Tensor, stream=None) -> None:
     """One token per unit: S <- e^g S + k v^T, o = q^T S.  q, k [B,H,d_k]; v, o [B,H,d_v]; g [B,H]."""
-    if q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {q.dtype}")
+    dev, dt = _device_of(q), q.dtype
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [B, H, d_k] and v [B, H, d_v]")
-    B, H, dk = q.shape
-    dv = v.shape[-1]
-    _expect(k, q.shape, "k")
-    _expect(v, (B, H, dv), "v")
-    _expect(o, v.shape, "o")
-    if g is not None:
-        _expect(g, (B, H), "g")
-    if state.numel() != B * H * dk * dv:
-        raise ValueError(f"state must hold {B * H} x {dk} x {dv} floats, got {state.numel()}")
-    dt = q.dtype
-    dev = _one_device(q=q, k=k, v=v, g=g, o=o, state=state)
-    _call("la_gated_decode_step", dev, stream, _ptr(q, "q", dt), _ptr(k, "k", dt), _ptr(v, "v", dt),
-          _ptr(g, "g", dt), _ptr(o, "o", dt), _ptr(state, "state", torch.float32), _DTYPES[dt], B, H, dk, dv)
+    qs = q.shape
+    B, H, dk = qs
+    dv = v.shape[2]
+    vs = (B, H, dv)
+    _run("la_gated_decode_step", dev, stream, _arg(q, "q", qs, dt, dev), _arg(k, "k", qs, dt, dev),
+         _arg(v, "v", vs, dt, dev), None if g is None else _arg(g, "g", (B, H), dt, dev), _arg(o, "o", vs, dt, dev),
+         _floats(state, "state", B * H * dk * dv, dev), _DTYPES[dt], B, H, dk, dv)
 
 
 def la_rotary_init(freq: torch.Tensor, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -387,8 +383,10 @@ def la_rotary_init(freq: torch.Tensor, base: float = 10000.0, scaling: str = "pl
         raise ValueError("freq must be [rot / 2]")
     if scaling not in ROTARY_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}, got {scaling!r}")
-    _call("la_rotary_init", freq.device, stream, _ptr(freq, "freq", torch.float32), 2 * freq.numel(), float(base),
-          ROTARY_SCALINGS[scaling], float(factor), float(original), float(beta_fast), float(beta_slow))
+    if freq.get_device() < 0:
+        raise ValueError("freq must be a CUDA tensor")
+    _run("la_rotary_init", freq.get_device(), stream, _ptr(freq, "freq", torch.float32), 2 * freq.numel(), base,
+         ROTARY_SCALINGS[scaling], factor, original, beta_fast, beta_slow)
 
 
 def la_rotary(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor, k_out: Optional[torch.Tensor],
@@ -397,25 +395,22 @@ def la_rotary(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor, k
               stream=None) -> None:
     """Turn the first 2 * len(freq) elements of every head by their positions.  q, k [B,H,T,d]; freq [rot / 2];
     start int32 [B] (or [num_seqs] with cu_seqlens): the first token's position.  The outputs may be the inputs."""
-    if q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {q.dtype}")
+    dev, dt = _device_of(q), q.dtype
     if q.dim() != 4:
         raise ValueError("q must be [B, H, T, d]")
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    B, H, T, d = q.shape
-    for name, t in (("k", k), ("q_out", q_out), ("k_out", k_out)):
-        if t is not None:
-            _expect(t, q.shape, name)
-    if freq.dim() != 1 or 2 * freq.numel() > d:
+    qs = q.shape
+    B, H, T, d = qs
+    rot = 2 * freq.numel()
+    if freq.dim() != 1 or rot > d:
         raise ValueError("freq must be [rot / 2] with rot <= d")
-    num_seqs = _packed(cu_seqlens, B)
-    if start is not None:
-        if start.dtype != torch.int32:
-            raise ValueError("start must be int32")
-        _expect(start, (num_seqs if cu_seqlens is not None else B,), "start")
-    dt = q.dtype
-    dev = _one_device(q=q, k=k, q_out=q_out, k_out=k_out, freq=freq, start=start, cu_seqlens=cu_seqlens)
-    _call("la_rotary", dev, stream, _ptr(q, "q", dt), _ptr(k, "k", dt), _ptr(q_out, "q_out", dt),
-          _ptr(k_out, "k_out", dt), _DTYPES[dt], B, H, T, d, 2 * freq.numel(), _ptr(freq, "freq", torch.float32),
-          _ptr(start, "start"), float(scale), int(interleaved), int(inverse), _ptr(cu_seqlens, "cu_seqlens"), num_seqs)
+    num_seqs, cu = 0, None
+    if cu_seqlens is not None:
+        num_seqs = _packed(cu_seqlens, B)
+        cu = _arg(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
+    _run("la_rotary", dev, stream, _arg(q, "q", qs, dt, dev), None if k is None else _arg(k, "k", qs, dt, dev),
+         _arg(q_out, "q_out", qs, dt, dev), None if k is None else _arg(k_out, "k_out", qs, dt, dev), _DTYPES[dt],
+         B, H, T, d, rot, _arg(freq, "freq", freq.shape, torch.float32, dev),
+         None if start is None else _arg(start, "start", (num_seqs if cu_seqlens is not None else B,), torch.int32, dev),
+         scale, interleaved, inverse, cu, num_seqs)

@@ -131,7 +131,8 @@ cudaError_t launch_gated_grad_simt(const GatedProblem& p, cudaStream_t s);
 constexpr int kGatedTcChunk = 128;
 struct GatedMaps {
     CUtensorMap q, k, v, d_o;       // loads: 64 columns x 128 rows
-    CUtensorMap o, dq, dk, dv;      // stores: 64 columns x 32 rows
+    CUtensorMap o;                  // stores: 64 columns x 32 rows
+    CUtensorMap dq, dk, dv;         // stores: 64 columns x 128 rows
 };
 // States at the chunk starts; with `grad` also the gradients at the chunk ends.
 cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s);

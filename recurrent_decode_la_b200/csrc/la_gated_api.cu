@@ -113,7 +113,8 @@ la_status maps(GatedMaps& m, const GatedProblem& p, bool grad) {
     };
     bool ok = enc(m.q, p.q, kGatedTcChunk) && enc(m.k, p.k, kGatedTcChunk) && enc(m.v, p.v, kGatedTcChunk);
     if (grad)
-        ok = ok && enc(m.d_o, p.d_o, kGatedTcChunk) && enc(m.dq, p.dq, 32) && enc(m.dk, p.dk_, 32) && enc(m.dv, p.dv_, 32);
+        ok = ok && enc(m.d_o, p.d_o, kGatedTcChunk) && enc(m.dq, p.dq, kGatedTcChunk) && enc(m.dk, p.dk_, kGatedTcChunk) &&
+             enc(m.dv, p.dv_, kGatedTcChunk);
     else
         ok = ok && enc(m.o, p.o, 32);
     return ok ? LA_OK : refuse(LA_ERR_CUDA, "cuTensorMapEncodeTiled failed");

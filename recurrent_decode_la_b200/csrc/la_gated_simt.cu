@@ -49,19 +49,32 @@ __device__ __forceinline__ void gate_prefix(const GatedProblem& p, int64_t row0,
 }
 
 // Rows row0 .. row0 + nv - 1 of x [.][d] into dst [C][kLd]; the rest zero.
+// Sixteen loads are in flight per thread before the first is stored.
 template <typename T>
 __device__ __forceinline__ void load_tile(float* dst, const void* x, int64_t row0, int nv, int d) {
     const T* X = static_cast<const T*>(x) + row0 * d;
-    for (int i = threadIdx.x; i < C * 128; i += kThreads) {
-        const int r = i >> 7, c = i & 127;
-        dst[r * kLd + c] = (r < nv && c < d) ? ld1(X, static_cast<int64_t>(r) * d + c) : 0.f;
+    const int c = threadIdx.x & 127, r0 = threadIdx.x >> 7;
+    float v[C / 2];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+        const int r = r0 + 2 * i;
+        v[i] = (r < nv && c < d) ? ld1(X, static_cast<int64_t>(r) * d + c) : 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) dst[(r0 + 2 * i) * kLd + c] = v[i];
 }
 
 __device__ __forceinline__ void load_state(float* dst, const float* src, int dk, int dv) {
-    for (int i = threadIdx.x; i < 128 * 128; i += kThreads) {
-        const int r = i >> 7, c = i & 127;
-        dst[r * kLd + c] = (r < dk && c < dv) ? src[r * dv + c] : 0.f;
+    const int c = threadIdx.x & 127, r0 = threadIdx.x >> 7;
+    for (int b = 0; b < 128; b += 32) {  // rows behind d_k zero: every row enters products
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = b + r0 + 2 * i;
+            v[i] = (r < dk && c < dv) ? src[r * dv + c] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[(b + r0 + 2 * i) * kLd + c] = v[i];
     }
 }
 
@@ -121,14 +134,15 @@ __device__ __forceinline__ void store_rows(void* y, int64_t row0, int nv, int d,
 // ---------------------------------------------------------------------------
 // State phase.  One CTA owns 32 of the d_v columns of a unit's state (a state
 // column depends on no other), in registers, 4 x 4 per thread, and walks the
-// chunks.  Forward: X = K weighted by e^{G_C - G_j}, Y = V.  Reverse: X = Q
-// weighted by e^{G_i}, Y = dO.
+// chunks; the next chunk's rows are loaded while one is computed.  Forward:
+// X = K, Y = V, weights e^{G_C - G_j}.  Reverse: X = Q, Y = dO, weights
+// e^{G_i}.  The weights go to Y, the smaller tile.
 // ---------------------------------------------------------------------------
 template <typename T, bool REV>
 __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const GatedProblem p, int col_blocks) {
     __shared__ float X[C][132];
-    __shared__ float Y[C][32];
-    __shared__ double G[C];
+    __shared__ float Y[C][36];
+    __shared__ double G[2][C];
     const int tid = threadIdx.x;
     const int64_t u = blockIdx.x / col_blocks;
     const int c0 = static_cast<int>(blockIdx.x % col_blocks) * 32;
@@ -149,42 +163,56 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
     const T* xs = static_cast<const T*>(REV ? p.q : p.k);
     const T* ys = static_cast<const T*>(REV ? p.d_o : p.v);
     const int nch = (un.len + C - 1) / C;
+    auto chunk = [&](int cc) { return REV ? nch - 1 - cc : cc; };
+    const int xc = tid & 127, xr = tid >> 7, yc = tid & 31, yr = tid >> 5;
+    float xv[C / 2], yv[C / 8];
+    auto fetch = [&](int cc) {  // chunk cc of the walk into registers, its prefix sums into G[cc & 1]
+        const int nv = min(C, un.len - chunk(cc) * C);
+        const int64_t row0 = un.row0 + static_cast<int64_t>(chunk(cc)) * C;
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            const int r = xr + 2 * i;
+            xv[i] = (r < nv && xc < dk) ? ld1(xs, (row0 + r) * dk + xc) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i) {
+            const int r = yr + 8 * i;
+            yv[i] = (r < nv && c0 + yc < dv) ? ld1(ys, (row0 + r) * dv + c0 + yc) : 0.f;
+        }
+        if (tid < 32) gate_prefix<T>(p, row0, nv, G[cc & 1]);
+    };
+    fetch(0);
     for (int cc = 0; cc < nch; ++cc) {
-        const int c = REV ? nch - 1 - cc : cc;
-        const int nv = min(C, un.len - c * C);
-        const int64_t row0 = un.row0 + static_cast<int64_t>(c) * C;
+        const int c = chunk(cc), nv = min(C, un.len - c * C);
+        __syncthreads();  // G is written; X and Y of the chunk before are read
+        const double* Gc = G[cc & 1];
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) X[xr + 2 * i][xc] = xv[i];
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i) {
+            const int r = yr + 8 * i;
+            Y[r][yc] = yv[i] * decay(REV ? Gc[r] : Gc[C - 1] - Gc[r]);
+        }
+        const float gamma = decay(Gc[C - 1]);
+        __syncthreads();
+        if (cc + 1 < nch) fetch(cc + 1);
         float* slot = slots + (un.slot0 + c) * usz;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < 4; ++m) {
                 if (r0 + i < dk && n0 + m < dv) slot[(r0 + i) * dv + n0 + m] = S[i][m];
-        __syncthreads();
-        if (tid < 32) gate_prefix<T>(p, row0, nv, G);
-        for (int i = tid; i < C * 32; i += kThreads) {
-            const int r = i >> 5, n = c0 + (i & 31);
-            Y[r][i & 31] = (r < nv && n < dv) ? ld1(ys, (row0 + r) * dv + n) : 0.f;
-        }
-        __syncthreads();
-        for (int i = tid; i < C * 128; i += kThreads) {
-            const int r = i >> 7, d = i & 127;
-            const float w = decay(REV ? G[r] : G[C - 1] - G[r]);
-            X[r][d] = (r < nv && d < dk) ? w * ld1(xs, (row0 + r) * dk + d) : 0.f;
-        }
-        const float gamma = decay(G[C - 1]);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) S[i][m] *= gamma;
+                S[i][m] *= gamma;
+            }
+#pragma unroll 4
         for (int j = 0; j < nv; ++j) {
             const float4 x = *reinterpret_cast<const float4*>(&X[j][r0]);
             const float4 y = *reinterpret_cast<const float4*>(&Y[j][n0 - c0]);
-            const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+            const float xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) S[i][m] = fmaf(xv[i], yv[m], S[i][m]);
+                for (int m = 0; m < 4; ++m) S[i][m] = fmaf(xa[i], ya[m], S[i][m]);
         }
     }
     if (out) {

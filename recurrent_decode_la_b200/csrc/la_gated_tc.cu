@@ -17,8 +17,8 @@
 // Rounding.  Sums, states and decays are fp32.  An operand of a product is
 // rounded to bf16 once where its result is bf16 too (decayed scores, chunk
 // states).  Where the result is an fp32 state, the decayed keys (queries) are
-// kept as the sum of two bf16 numbers, 2^-16 of them, at the price of a second
-// product.  A row's decay is applied to the fp32 accumulator, not to a bf16
+// kept as the sum of three bf16 numbers, 2^-24 of them, at the price of two
+// more products (two parts would leave the state 2.5e-6 of itself off).  A row's decay is applied to the fp32 accumulator, not to a bf16
 // operand.  The tensor core drops bits when it adds to an accumulator: a state
 // summed there over 8192 tokens is off by 9e-6 of itself, so the states live in
 // registers and an accumulator spans one chunk only.
@@ -124,6 +124,17 @@ __device__ __forceinline__ void ld32f(uint32_t taddr, float (&x)[32]) {
     }
 }
 
+__device__ __forceinline__ void ld16f(uint32_t taddr, float (&x)[16]) {
+    uint32_t r[16];
+    tmem_ld16(taddr, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        asm volatile("" : "+r"(r[i]));
+        x[i] = __uint_as_float(r[i]);
+    }
+}
+
 __device__ __forceinline__ uint32_t tile_k(uint32_t tile, int ks, uint32_t panel) {  // K-major step ks
     return tile + (ks >> 2) * panel + (ks & 3) * 32;
 }
@@ -131,36 +142,47 @@ __device__ __forceinline__ uint32_t tile_k(uint32_t tile, int ks, uint32_t panel
 // ---------------------------------------------------------------------------
 // States.  Work item i < n_units: unit i forward, X = K, Y = V; the others
 // (gradient): unit i - n_units in reverse, X = Q, Y = dO.  Per chunk
-//     U = X'^T Y (X' = the decayed rows, as a high and a low bf16 part),
+//     U = X'^T Y (X' = the decayed rows, as the sum of three bf16 numbers),
 //     S = gamma S + U.
 //   warp 0       TMA producer        warp 1  MMA issuer
 //   warp 2       decays of the chunk's tokens
-//   warps 4-7    X -> high part in place, low part beside it
-//   warps 8-15   (8-11 at D = 64) the state, 64 columns of a row per thread
+//   warps 4-11   X -> its three decayed parts.  At D = 128 transposed into
+//                tensor memory, whence the product takes them: with the parts
+//                in shared memory its bandwidth (parts written and read, 3.6k
+//                clocks a chunk) binds.  At D = 64 in shared memory, the high
+//                part in place.
+//   warps 12-19  (12-15 at D = 64) the state, 64 columns of a row per thread
 // ---------------------------------------------------------------------------
 template <int D>
 struct StCfg {
-    static constexpr int kThreads = 512;
+    static constexpr int kThreads = 640;
     static constexpr int NPAN = D / 64;
     static constexpr int TILE = C * D * 2;
-    static constexpr int STAGE = 3 * TILE;  // X (then its high part), Y, low part of X
-    static constexpr int NS = D == 128 ? 2 : 4;
+    static constexpr bool TS = D == 128;    // decayed parts in tensor memory
+    static constexpr int STAGE = 2 * TILE;  // X, Y
+    static constexpr int NS = D == 128 ? 3 : 4;
+    static constexpr int NL = 2;            // buffers of the decayed parts
+    static constexpr int NU = TS ? 1 : 2;   // accumulators
     static constexpr int SB = D * D * 2, SB_PANEL = D * 128;
-    static constexpr int kGam = 8;  // live gammas: NS + 2 chunks at most
-    static constexpr int OFF_SB = NS * STAGE;
+    static constexpr int kGam = 8;  // live gammas: those of at most six chunks
+    static constexpr int OFF_LO = NS * STAGE;
+    static constexpr int OFF_SB = OFF_LO + (TS ? 0 : NL * 2 * TILE);
     static constexpr int OFF_W = OFF_SB + SB;
-    static constexpr int OFF_GAM = OFF_W + NS * C * 4;
+    static constexpr int NW = 2;            // sets of decays, each [3][128] bf16: w = w0 + w1 + w2
+    static constexpr int OFF_GAM = OFF_W + NW * 3 * C * 2;
     static constexpr int OFF_BAR = OFF_GAM + kGam * 4;
     static constexpr int B_FULL = 0, B_EMPTY = NS, B_GFULL = 2 * NS, B_SCALED = 3 * NS, B_UFULL = 4 * NS,
-                         B_UEMPTY = 4 * NS + 2, B_DONE = 4 * NS + 4, NBAR = 4 * NS + 5;
+                         B_UEMPTY = 4 * NS + NU, B_DONE = 4 * NS + 2 * NU, B_LOEMPTY = B_DONE + 1, NBAR = B_DONE + 1 + NL;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
-    static constexpr int TM_COLS = 2 * D;
-    static_assert(SMEM <= 232448 && NS + 2 <= kGam, "shared memory");
+    static constexpr int TM_COLS = TS ? 512 : 2 * D;
+    // columns of part k of buffer l (TS)
+    static constexpr int tm_part(int l, int k) { return NU * D + (l * 3 + k) * 64; }
+    static_assert(SMEM <= 232448, "shared memory");
 };
 
 template <int D>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(640, 1)
     gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items) {
     using Cfg = StCfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -169,7 +191,6 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
-    float* wts = reinterpret_cast<float*>(smem + Cfg::OFF_W);
     float* gam = reinterpret_cast<float*>(smem + Cfg::OFF_GAM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.timeout_ns;
@@ -180,13 +201,14 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(&bar[Cfg::B_FULL + s], 1);
             mbar_init(&bar[Cfg::B_EMPTY + s], 1);
             mbar_init(&bar[Cfg::B_GFULL + s], 1);
-            mbar_init(&bar[Cfg::B_SCALED + s], 4);
+            mbar_init(&bar[Cfg::B_SCALED + s], 8);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < Cfg::NU; ++b) {
             mbar_init(&bar[Cfg::B_UFULL + b], 1);
             mbar_init(&bar[Cfg::B_UEMPTY + b], 4 * Cfg::NPAN);
         }
         mbar_init(&bar[Cfg::B_DONE], 1);
+        for (int l = 0; l < Cfg::NL; ++l) mbar_init(&bar[Cfg::B_LOEMPTY + l], 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -256,23 +278,33 @@ __global__ void __launch_bounds__(512, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t kId = idesc_bf16_f32(D, D, true, true);
+            constexpr uint32_t kId = idesc_bf16_f32(D, D, !Cfg::TS, true);
             bool issued = false;
             walk([&](const GatedUnit&, bool, int, int, int64_t g) {
-                const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
+                const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g % Cfg::NU), l = static_cast<int>(g % Cfg::NL);
                 if (!mbar_wait(&bar[Cfg::B_SCALED + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x610 + s)) return false;
-                if (g >= 2 && !mbar_wait(&bar[Cfg::B_UEMPTY + b], ((g >> 1) + 1) & 1, abort_flag, tmo, 0x618 + b))
+                if (g >= Cfg::NU &&
+                    !mbar_wait(&bar[Cfg::B_UEMPTY + b], ((g / Cfg::NU) + 1) & 1, abort_flag, tmo, 0x618 + b))
                     return false;
                 tc_fence_after();
-                const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE, lo = y + Cfg::TILE;
+                const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE,
+                               lo = sbase + Cfg::OFF_LO + l * 2 * Cfg::TILE;
+                // the smallest part first
 #pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks)
-                    mma_bf16_ss(tmem + b * D, sdesc_sw128(lo + ks * 2048, kPanel, 1024),
-                                sdesc_sw128(y + ks * 2048, kPanel, 1024), kId, ks > 0);
+                for (int part = 2; part >= 0; --part) {
 #pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks)
-                    mma_bf16_ss(tmem + b * D, sdesc_sw128(x + ks * 2048, kPanel, 1024),
-                                sdesc_sw128(y + ks * 2048, kPanel, 1024), kId, 1);
+                    for (int ks = 0; ks < C / 16; ++ks) {
+                        const uint64_t yd = sdesc_sw128(y + ks * 2048, kPanel, 1024);
+                        const uint32_t acc = part < 2 || ks > 0;
+                        if constexpr (Cfg::TS)
+                            mma_bf16_ts(tmem + b * D, tmem + Cfg::tm_part(l, part) + ks * 8, yd, kId, acc);
+                        else
+                            mma_bf16_ss(tmem + b * D,
+                                        sdesc_sw128((part == 0 ? x : lo + (part - 1) * Cfg::TILE) + ks * 2048, kPanel, 1024),
+                                        yd, kId, acc);
+                    }
+                    if (part == (Cfg::TS ? 0 : 1)) mma_commit(&bar[Cfg::B_LOEMPTY + l]);
+                }
                 mma_commit(&bar[Cfg::B_EMPTY + s]);
                 mma_commit(&bar[Cfg::B_UFULL + b]);
                 issued = true;
@@ -295,44 +327,114 @@ __global__ void __launch_bounds__(512, 1)
             } else {
                 scan_down(x, w, all);
             }
-            if (g >= Cfg::NS &&
-                !mbar_wait_warp(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x620 + s))
+            if (g >= 2 && !mbar_wait_warp(&bar[Cfg::B_SCALED + (g - 2) % Cfg::NS], ((g - 2) / Cfg::NS) & 1, abort_flag,
+                                          tmo, 0x620 + s))
                 return false;
-            reinterpret_cast<float4*>(wts + s * C)[lane] = make_float4(ex2(w[0]), ex2(w[1]), ex2(w[2]), ex2(w[3]));
+            uint2* o = reinterpret_cast<uint2*>(smem + Cfg::OFF_W + (g % Cfg::NW) * 3 * C * 2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = ex2(w[e]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const uint2 h = make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
+                o[32 * k + lane] = h;
+                w[0] -= bf16_lo(h.x);
+                w[1] -= bf16_hi(h.x);
+                w[2] -= bf16_lo(h.y);
+                w[3] -= bf16_hi(h.y);
+            }
             if (lane == 0) gam[g % Cfg::kGam] = ex2(all);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
             return true;
         });
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4 && warp < 12) {
         walk([&](const GatedUnit&, bool, int, int nv, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
             const uint32_t ph = (g / Cfg::NS) & 1;
             if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], ph, abort_flag, tmo, 0x630 + s)) return false;
             if (!mbar_wait_warp(&bar[Cfg::B_FULL + s], ph, abort_flag, tmo, 0x638 + s)) return false;
-            const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE, lo = y + Cfg::TILE;
-            const float* w = wts + s * C;
-            // warp w takes rows 32 (w - 4) ..; its lanes four rows of eight 16-byte pieces at a time
-            const int r0 = (warp - 4) * 32 + (lane >> 3);
-#pragma unroll 2
-            for (int it = 0; it < 8; ++it) {
-                const int row = r0 + 4 * it;
-                const float f = w[row];
+            const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE;
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + Cfg::OFF_W + (g % Cfg::NW) * 3 * C * 2);
+            // w x = hi + mid + lo for two values at a time, in paired bf16 arithmetic.  A product of two 8-bit
+            // significands has 16 bits, so w0 x = hi + r and w1 x = p + e1 exactly; r + p = mid + e2 exactly; what
+            // follows is rounded, 2^-26 of w x.
+            auto split = [](uint32_t x2, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+                auto b = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
+                auto u = [](__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); };
+                const __nv_bfloat162 x = b(x2), h = __hmul2_rn(b(w0), x), r = __hfma2(b(w0), x, __hneg2(h)),
+                                     p = __hmul2_rn(b(w1), x), e1 = __hfma2(b(w1), x, __hneg2(p)), m = __hadd2_rn(r, p),
+                                     q = __hsub2_rn(m, r),
+                                     e2 = __hadd2_rn(__hsub2_rn(r, __hsub2_rn(m, q)), __hsub2_rn(p, q));
+                hi = u(h);
+                mid = u(m);
+                lo = u(__hfma2(b(w2), x, __hadd2_rn(e1, e2)));
+            };
+            const bool lofree = g < Cfg::NL;
+            const uint32_t loph = ((g / Cfg::NL) + 1) & 1;
+            if constexpr (Cfg::TS) {
+                // lanes = columns of X: this warp's 32 of them, in two groups of 16, and 64 of the tokens
+                const int sub = warp & 3, half = (warp - 4) >> 2;
+                if (nv < C)
+                    for (int row = nv + (warp - 4); row < C; row += 8)
+                        if (lane < 16) st_shared_v4(y + (lane >> 3) * kPanel + row * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int pn = 0; pn < Cfg::NPAN; ++pn) {
-                    const uint32_t at = pn * kPanel + row * 128 + (lane & 7) * 16;
-                    uint32_t a[4], hi[4], l[4];
-                    ld_shared_v4(x + at, a[0], a[1], a[2], a[3]);
+                for (int grp = 0; grp < 2; ++grp) {
+                    uint32_t part[3][16];
+                    const int c0 = 4 * sub + 2 * grp;  // first 16-byte piece of the 16 columns
+                    const uint32_t panel = x + (c0 >> 3) * kPanel;
+                    const int tok = 64 * half + (lane & 7) + ((lane >> 4) << 3), ch = (c0 & 7) + ((lane >> 3) & 1);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float u0 = f * bf16_lo(a[e]), u1 = f * bf16_hi(a[e]);
-                        hi[e] = pack_bf16x2(u0, u1);
-                        l[e] = pack_bf16x2(u0 - bf16_lo(hi[e]), u1 - bf16_hi(hi[e]));
-                        if (row >= nv) hi[e] = l[e] = 0u;
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t a[4];
+                        ldmatrix_x4_trans(panel + sw128_off(tok + 16 * k, ch), a[0], a[1], a[2], a[3]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int t0 = 64 * half + 16 * k + 8 * (r >> 1) + 2 * (lane & 3);
+                            uint32_t v = a[r];
+                            if (nv < C) v &= (t0 < nv ? 0xffffu : 0u) | (t0 + 1 < nv ? 0xffff0000u : 0u);
+                            split(v, w[t0 >> 1], w[64 + (t0 >> 1)], w[128 + (t0 >> 1)], part[0][4 * k + r], part[1][4 * k + r], part[2][4 * k + r]);
+                        }
                     }
+                    if (grp == 0) {
+                        if (!lofree && !mbar_wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
+                            return false;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        tmem_st_16x128b_x8(tmem + Cfg::tm_part(g % Cfg::NL, k) + half * 32 +
+                                               (static_cast<uint32_t>(sub * 32 + grp * 16) << 16),
+                                           part[k]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+            } else {
+                const uint32_t lo = sbase + Cfg::OFF_LO + (g % Cfg::NL) * 2 * Cfg::TILE;
+                if (!lofree && !mbar_wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
+                    return false;
+                // warp w takes rows 16 (w - 4) ..; its lanes four rows of eight 16-byte pieces at a time
+                const int r0 = (warp - 4) * 16 + (lane >> 3);
+                uint32_t a[4][4];
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+                    ld_shared_v4(x + (r0 + 4 * it) * 128 + (lane & 7) * 16, a[it][0], a[it][1], a[it][2], a[it][3]);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int row = r0 + 4 * it;
+                    const uint32_t at = row * 128 + (lane & 7) * 16;
+                    uint32_t hi[4], l[4], l2[4], wr[3];
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {  // the row's decay in both halves
+                        const uint32_t both = w[64 * k + (row >> 1)];
+                        wr[k] = __byte_perm(both, 0u, row & 1 ? 0x3232 : 0x1010);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        split(row < nv ? a[it][e] : 0u, wr[0], wr[1], wr[2], hi[e], l[e], l2[e]);
+                    if (row >= nv) st_shared_v4(y + at, 0u, 0u, 0u, 0u);
                     st_shared_v4(x + at, hi[0], hi[1], hi[2], hi[3]);
                     st_shared_v4(lo + at, l[0], l[1], l[2], l[3]);
-                    if (row >= nv) st_shared_v4(y + at, 0u, 0u, 0u, 0u);
+                    st_shared_v4(lo + Cfg::TILE + at, l2[0], l2[1], l2[2], l2[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -340,8 +442,8 @@ __global__ void __launch_bounds__(512, 1)
             if (lane == 0) mbar_arrive(&bar[Cfg::B_SCALED + s]);
             return true;
         });
-    } else if (warp >= 8 && warp < 8 + 4 * Cfg::NPAN) {
-        const int sub = warp & 3, half = (warp - 8) >> 2;
+    } else if (warp >= 12 && warp < 12 + 4 * Cfg::NPAN) {
+        const int sub = warp & 3, half = (warp - 12) >> 2;
         const int row = D == 128 ? sub * 32 + lane : (lane < 16 ? sub * 16 + lane : -1);
         const uint32_t lane_off = (static_cast<uint32_t>(sub * 32) << 16) + half * 64;
         uint8_t* panel = smem + Cfg::OFF_SB + half * Cfg::SB_PANEL;
@@ -369,7 +471,7 @@ __global__ void __launch_bounds__(512, 1)
             uint8_t* slots = static_cast<uint8_t*>(rev ? p.e_states : p.s_states) + un.slot0 * Cfg::SB;
             for (int cc = 0; cc < nch; ++cc, ++g) {
                 const int c = rev ? nch - 1 - cc : cc;
-                const int b = static_cast<int>(g & 1);
+                const int b = static_cast<int>(g % Cfg::NU);
                 // the state before this chunk, as bf16, to its slot
                 if (lane == 0) bulk_wait_group_read<0>();
                 __syncwarp();
@@ -388,18 +490,18 @@ __global__ void __launch_bounds__(512, 1)
                     bulk_store(slots + static_cast<int64_t>(c) * Cfg::SB + off, smem + Cfg::OFF_SB + off, kRows * 128);
                     bulk_commit_group();
                 }
-                if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x640 + b)) {
+                if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const float gamma = gam[g % Cfg::kGam];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[32];
-                    ld32f(tmem + lane_off + b * D + h * 32, x);
+                for (int h = 0; h < 4; ++h) {
+                    float x[16];
+                    ld16f(tmem + lane_off + b * D + h * 16, x);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) S[h * 32 + j] = fmaf(gamma, S[h * 32 + j], x[j]);
+                    for (int j = 0; j < 16; ++j) S[h * 16 + j] = fmaf(gamma, S[h * 16 + j], x[j]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -429,14 +531,16 @@ __global__ void __launch_bounds__(512, 1)
 // The decay of a whole 32 x 32 block left of the diagonal is the product of a
 // column's factor, e^{R - G_j} with R the prefix at the block's end, and a
 // row's, e^{G_i - R}; only the diagonal blocks take an exponential per element.
-//   warp 0       TMA producer        warp 1  MMA issuer
+//   warp 0       TMA producer        warps 1, 3  MMA issuers (output; scores,
+//                which must not wait behind the output of the chunk before)
 //   warp 2       decays; zeroes the rows behind a sequence's end in V
-//   warps 4-7    scores -> P (bf16, over the scores in tensor memory)
-//   warps 8-15   (8-11 at D = 64) O -> bf16, staged in the chunk's Q tile -> TMA store
+//   warps 4-11   scores -> P (bf16, over the scores in tensor memory); two warps
+//                share 32 rows, 64 keys each
+//   warps 12-19  (12-15 at D = 64) O -> bf16, staged in the chunk's Q tile -> TMA store
 // ---------------------------------------------------------------------------
 template <int D>
 struct OutCfg {
-    static constexpr int kThreads = 512;
+    static constexpr int kThreads = 640;
     static constexpr int NPAN = D / 64;
     static constexpr int TILE = C * D * 2;
     static constexpr int STAGE = 3 * TILE;
@@ -448,7 +552,7 @@ struct OutCfg {
     static constexpr int OFF_BAR = OFF_G + NS * G_BYTES;
     static constexpr int B_FULL = 0, B_EMPTY = NS, B_GFULL = 2 * NS, B_SFULL = 3 * NS, B_SEMPTY = 3 * NS + 1,
                          B_AFULL = 3 * NS + 2, B_PFULL = 3 * NS + 4, B_OFULL = 3 * NS + 6, B_OEMPTY = 3 * NS + 7,
-                         B_DONE = 3 * NS + 8, NBAR = 3 * NS + 9;
+                         B_DONE = 3 * NS + 8, B_PEMPTY = 3 * NS + 10, NBAR = 3 * NS + 12;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TM_A = 0, TM_O1 = 256, TM_O2 = 256 + D;
@@ -456,7 +560,7 @@ struct OutCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(640, 1)
     gated_out_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_slots) {
     using Cfg = OutCfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -479,11 +583,13 @@ __global__ void __launch_bounds__(512, 1)
         mbar_init(&bar[Cfg::B_SEMPTY], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bar[Cfg::B_AFULL + b], 1);
-            mbar_init(&bar[Cfg::B_PFULL + b], 4);
+            mbar_init(&bar[Cfg::B_PFULL + b], 8);
+            mbar_init(&bar[Cfg::B_PEMPTY + b], 1);
         }
         mbar_init(&bar[Cfg::B_OFULL], 1);
         mbar_init(&bar[Cfg::B_OEMPTY], 4 * Cfg::NPAN);
         mbar_init(&bar[Cfg::B_DONE], 1);
+        mbar_init(&bar[Cfg::B_DONE + 1], 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -529,6 +635,20 @@ __global__ void __launch_bounds__(512, 1)
                 mbar_arrive_expect_tx(&bar[Cfg::B_SFULL], Cfg::SB);
                 bulk_load(smem + Cfg::OFF_SB, static_cast<const uint8_t*>(p.s_states) + slot * Cfg::SB, Cfg::SB,
                           &bar[Cfg::B_SFULL]);
+                // the next chunk into L2, while its stage is still in use
+                const int64_t next = slot + gridDim.x;
+                if (next < n_slots) {
+                    const GatedChunk c2 = gated_chunk(p, next, C);
+                    if (c2.nv > 0) {
+#pragma unroll
+                        for (int pn = 0; pn < Cfg::NPAN; ++pn) {
+                            tma_prefetch_l2_3d(&m.q, pn * 64, c2.row, c2.group);
+                            tma_prefetch_l2_3d(&m.k, pn * 64, c2.row, c2.group);
+                            tma_prefetch_l2_3d(&m.v, pn * 64, c2.row, c2.group);
+                        }
+                        bulk_prefetch_l2(static_cast<const uint8_t*>(p.s_states) + next * Cfg::SB, Cfg::SB);
+                    }
+                }
                 return true;
             });
             if (!ok || *abort_flag) {
@@ -539,7 +659,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (ok && started >= 1) mbar_wait_drain(&bar[Cfg::B_SFULL], (started - 1) & 1, tmo);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
         if (lane == 0) {
             constexpr uint32_t kIdA = idesc_bf16_f32(C, C, false, false);
             constexpr uint32_t kIdO = idesc_bf16_f32(C, D, false, true);
@@ -547,8 +667,8 @@ __global__ void __launch_bounds__(512, 1)
             auto scores = [&](int64_t g) -> bool {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
                 if (!mbar_wait(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x710 + s)) return false;
-                // the buffer's last P was read by the product of chunk g - 2, which O of that chunk waited for
-                if (g >= 2 && !mbar_wait(&bar[Cfg::B_OFULL], (g - 2) & 1, abort_flag, tmo, 0x718)) return false;
+                // the buffer's last P, of chunk g - 2, is used up
+                if (g >= 2 && !mbar_wait(&bar[Cfg::B_PEMPTY + b], ((g >> 1) + 1) & 1, abort_flag, tmo, 0x718)) return false;
                 tc_fence_after();
                 const uint32_t q = sbase + s * Cfg::STAGE, k = q + Cfg::TILE;
 #pragma unroll
@@ -562,6 +682,7 @@ __global__ void __launch_bounds__(512, 1)
             auto output = [&](int64_t g) -> bool {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
                 if (g >= 1 && !mbar_wait(&bar[Cfg::B_OEMPTY], (g + 1) & 1, abort_flag, tmo, 0x720)) return false;
+                if (!mbar_wait(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x724)) return false;
                 if (!mbar_wait(&bar[Cfg::B_SFULL], g & 1, abort_flag, tmo, 0x728)) return false;
                 tc_fence_after();
                 const uint32_t q = sbase + s * Cfg::STAGE, v = q + 2 * Cfg::TILE, sb = sbase + Cfg::OFF_SB;
@@ -570,27 +691,24 @@ __global__ void __launch_bounds__(512, 1)
                     mma_bf16_ss(tmem + Cfg::TM_O1, sdesc_sw128(tile_k(q, ks, kPanel), 16, 1024),
                                 sdesc_sw128(sb + ks * 2048, Cfg::SB_PANEL, 1024), kIdO, ks > 0);
                 mma_commit(&bar[Cfg::B_SEMPTY]);
+                issued = true;
                 if (!mbar_wait(&bar[Cfg::B_PFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x730 + b)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks)
-                    mma_bf16_ts(tmem + Cfg::TM_O2, tmem + Cfg::TM_A + b * C + ks * 8,
+                    mma_bf16_ts(tmem + Cfg::TM_O2, tmem + Cfg::TM_A + b * C + (ks >> 2) * 64 + (ks & 3) * 8,
                                 sdesc_sw128(v + ks * 2048, kPanel, 1024), kIdO, ks > 0);
+                mma_commit(&bar[Cfg::B_PEMPTY + b]);
                 mma_commit(&bar[Cfg::B_OFULL]);
                 return true;
             };
-            // the scores run one chunk ahead of the output
-            int64_t last = -1;
-            bool ok = walk([&](const GatedChunk&, int64_t, int64_t g) {
-                if (!scores(g)) return false;
-                if (g >= 1 && !output(g - 1)) return false;
-                last = g;
-                return true;
-            });
-            if (ok && last >= 0) output(last);
+            if (warp == 3)
+                walk([&](const GatedChunk&, int64_t, int64_t g) { return scores(g); });
+            else
+                walk([&](const GatedChunk&, int64_t, int64_t g) { return output(g); });
             if (issued) {
-                mma_commit(&bar[Cfg::B_DONE]);
-                mbar_wait_drain(&bar[Cfg::B_DONE], 0, tmo);
+                mma_commit(&bar[Cfg::B_DONE + (warp == 3)]);
+                mbar_wait_drain(&bar[Cfg::B_DONE + (warp == 3)], 0, tmo);
             }
         }
         __syncwarp();
@@ -614,8 +732,8 @@ __global__ void __launch_bounds__(512, 1)
             if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
             return true;
         });
-    } else if (warp >= 4 && warp < 8) {
-        const int sub = warp & 3, row = sub * 32 + lane;
+    } else if (warp >= 4 && warp < 12) {
+        const int sub = warp & 3, half = (warp - 4) >> 2, row = sub * 32 + lane;
         walk([&](const GatedChunk&, int64_t, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
             if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x750 + s)) return false;
@@ -623,53 +741,50 @@ __global__ void __launch_bounds__(512, 1)
             tc_fence_after();
             const float* G = reinterpret_cast<const float*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES);
             const float* F = G + C;
-            const uint32_t tm = tmem + Cfg::TM_A + b * C + (static_cast<uint32_t>(sub * 32) << 16);
+            // scores of this half's keys in columns 64 half ..; P goes to the first 32 of them
+            const uint32_t tm = tmem + Cfg::TM_A + b * C + half * 64 + (static_cast<uint32_t>(sub * 32) << 16);
             const float Gi = G[row];
-            // half h of the keys: scores in columns 64 h .., P written to columns 32 h .. (already read)
+            uint32_t w[32];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t w[32];
+            for (int q = 0; q < 2; ++q) {
+                const int jb = 2 * half + q;  // block of 32 keys; warp-uniform cases
+                if (jb > sub) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int jb = 2 * h + q;  // block of 32 keys; warp-uniform cases
-                    if (jb > sub) {
+                    for (int e = 0; e < 16; ++e) w[16 * q + e] = 0u;
+                    continue;
+                }
+                float a[32];
+                ld32f(tm + q * 32, a);
+                if (jb < sub) {
+                    const float f = ex2(Gi - G[jb * 32 + 31]);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) w[16 * q + e] = 0u;
-                        continue;
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 c = reinterpret_cast<const float4*>(F + jb * 32)[e];
+                        w[16 * q + 2 * e] = pack_bf16x2(a[4 * e] * (f * c.x), a[4 * e + 1] * (f * c.y));
+                        w[16 * q + 2 * e + 1] = pack_bf16x2(a[4 * e + 2] * (f * c.z), a[4 * e + 3] * (f * c.w));
                     }
-                    float a[32];
-                    ld32f(tm + jb * 32, a);
-                    if (jb < sub) {
-                        const float f = ex2(Gi - G[jb * 32 + 31]);
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float4 c = reinterpret_cast<const float4*>(F + jb * 32)[e];
-                            w[16 * q + 2 * e] = pack_bf16x2(a[4 * e] * (f * c.x), a[4 * e + 1] * (f * c.y));
-                            w[16 * q + 2 * e + 1] = pack_bf16x2(a[4 * e + 2] * (f * c.z), a[4 * e + 3] * (f * c.w));
-                        }
-                    } else {
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 c = reinterpret_cast<const float4*>(G + jb * 32)[e];
+                        const float d[4] = {c.x, c.y, c.z, c.w};
+                        float y[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float4 c = reinterpret_cast<const float4*>(G + jb * 32)[e];
-                            const float d[4] = {c.x, c.y, c.z, c.w};
-                            float y[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) y[k] = 4 * e + k <= lane ? a[4 * e + k] * ex2(Gi - d[k]) : 0.f;
-                            w[16 * q + 2 * e] = pack_bf16x2(y[0], y[1]);
-                            w[16 * q + 2 * e + 1] = pack_bf16x2(y[2], y[3]);
-                        }
+                        for (int k = 0; k < 4; ++k) y[k] = 4 * e + k <= lane ? a[4 * e + k] * ex2(Gi - d[k]) : 0.f;
+                        w[16 * q + 2 * e] = pack_bf16x2(y[0], y[1]);
+                        w[16 * q + 2 * e + 1] = pack_bf16x2(y[2], y[3]);
                     }
                 }
-                tmem_st32(tm + h * 32, w);
             }
+            tmem_st32(tm, w);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_PFULL + b]);
             return true;
         });
-    } else if (warp >= 8 && warp < 8 + 4 * Cfg::NPAN) {
-        const int sub = warp & 3, half = (warp - 8) >> 2, row = sub * 32 + lane;
+    } else if (warp >= 12 && warp < 12 + 4 * Cfg::NPAN) {
+        const int sub = warp & 3, half = (warp - 12) >> 2, row = sub * 32 + lane;
         const uint32_t lane_off = (static_cast<uint32_t>(sub * 32) << 16) + half * 64;
         walk([&](const GatedChunk& ch, int64_t, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
@@ -729,22 +844,24 @@ __global__ void __launch_bounds__(512, 1)
 //     T3 = e^{G_C - G_j} (V E^T) + W^T Q -> dk
 //     T1 = e^{G_C - G_j} (K E) + P^T dO  -> dv
 // Each decayed part is scaled in tensor memory before its second product is
-// accumulated onto it; on the way its dot product with q (k) gives the terms
-// of dg that pass a chunk's edge.  The terms within the chunk are row and
-// column sums of M = w (q k)(do v) in fp32: what gate t gets is
-// sum_{i >= t} (row_i - column_i), whose terms cancel exactly but for fp32.
+// accumulated onto it.  dg comes from the results, before they are rounded:
+// with cj = e^{G_C - G_j} k_j . (E v_j), taken when T3 is scaled,
+//     dg_t = e^{G_C} <E, S> + sum_{i >= t} (q_i . dq_i - k_i . dk_i + cj_i) + sum_{j < t} cj_j.
+// Within the chunk dq and dk are sums of the same rounded W_ij, so what a
+// token gives and what it takes cancel to fp32, and the sums restart at every
+// chunk.
 //   warp 0       producer            warp 1  MMA issuer
-//   warp 2       decays; zeroes the rows behind a sequence's end
-//   warp 3       dg
-//   warps 4-11   everything else: two warps share 32 rows, each takes half of
-//                the columns
+//   warp 2       decays; zeroes the rows behind a sequence's end; stores dv
+//   warp 3       dg; stores dq and dk
+//   warps 4-19   everything else: four warps share 32 rows, 32 columns each (at
+//                D = 64 two of them work on the D-wide tiles)
 // Tiles are loaded once each (one stage at D = 128: 192 KB), reloaded for the
-// next chunk as each dies, and dq, dk, dv are staged for their stores in the
-// dead tiles of K, Q and dO.
+// next chunk as each dies; W^T lies over V, and dq, dk, dv are staged for their
+// stores in the tiles of q, k and dO.
 // ---------------------------------------------------------------------------
 template <int D>
 struct GrCfg {
-    static constexpr int kThreads = 384;
+    static constexpr int kThreads = 640;
     static constexpr int NPAN = D / 64;
     static constexpr int TILE = C * D * 2;
     static constexpr int SB = D * D * 2, SB_PANEL = D * 128;
@@ -753,73 +870,66 @@ struct GrCfg {
     // tiles of a stage
     static constexpr int Q = 0, K = TILE, V = 2 * TILE, O = 3 * TILE, S = 4 * TILE, E = 4 * TILE + SB;
     static constexpr int W_BYTES = C * C * 2;
-    // W^T: over S at D = 128 (S is dead by then), a tile of its own at D = 64
-    static constexpr int OFF_W = D == 128 ? S : NS * STAGE;
+    // W^T: over V at D = 128 (V is dead by then), a tile of its own at D = 64
+    static constexpr int OFF_W = D == 128 ? V : NS * STAGE;
     static constexpr int OFF_G = NS * STAGE + (D == 128 ? 0 : W_BYTES);
     // [2][4][128]: prefix sums; e^{G_i}; e^{G_C - G_j}; e^{G_i - R}, R the prefix before i's block
-    static constexpr int OFF_ROWS = OFF_G + 2 * 4 * C * 4;  // sum_j M by block of 32 keys [4][128]
-    static constexpr int OFF_COLS = OFF_ROWS + 4 * C * 4;   // sum_i M by half [2][128]
-    static constexpr int OFF_RI = OFF_COLS + 2 * C * 4;     // e^{G_i} q_i . S do_i by half [2][128]
-    static constexpr int OFF_CJ = OFF_RI + 2 * C * 4;       // e^{G_C - G_j} k_j . E v_j by half [2][128]
-    static constexpr int OFF_ES = OFF_CJ + 2 * C * 4;       // e^{G_C} <E, S> by warp [8]
-    static constexpr int OFF_BAR = OFF_ES + 32;
+    static constexpr int NQ = D / 32;                       // warps with columns of the D-wide tiles, per 32 rows
+    static constexpr int OFF_U = OFF_G + 2 * 4 * C * 4;  // q_i . dq_i - k_i . dk_i by 32 columns [NQ][128]
+    static constexpr int OFF_CJ = OFF_U + NQ * C * 4;    // e^{G_C - G_j} k_j . E v_j by 32 columns [NQ][128]
+    static constexpr int OFF_ES = OFF_CJ + NQ * C * 4;   // e^{G_C} <E, S> by warp [16]
+    static constexpr int OFF_BAR = OFF_ES + 64;
     // per stage: loads and releases of Q, K, V, dO, S, E
     static constexpr int F_Q = 0, F_K = 1, F_V = 2, F_O = 3, F_S = 4, F_E = 5;
-    static constexpr int B_FULL = 0, B_EMPTY = 6 * NS, B_GFULL = 12 * NS, B_ABFULL = 12 * NS + NS, B_X = B_ABFULL + 1,
-                         B_Y = B_ABFULL + 2, B_Z = B_ABFULL + 3, B_P = B_ABFULL + 4, B_XYS = B_ABFULL + 5,
-                         B_ZS = B_ABFULL + 6, B_DQ = B_ABFULL + 7, B_DK = B_ABFULL + 8, B_DV = B_ABFULL + 9,
+    static constexpr int B_FULL = 0, B_EMPTY = 6 * NS, B_GFULL = 12 * NS, B_ABFULL = 12 * NS + NS, B_Y = B_ABFULL + 2, B_Z = B_ABFULL + 3, B_P = B_ABFULL + 4, B_XYS = B_ABFULL + 5,
+                         B_ZS = B_ABFULL + 6, B_DK = B_ABFULL + 8, B_DV = B_ABFULL + 9,
                          B_FREE = B_ABFULL + 10 /* T2, T3, T1 read out */, B_SUMS = B_ABFULL + 13,
                          B_SUMFREE = B_ABFULL + 14, B_DONE = B_ABFULL + 15, B_READ = B_ABFULL + 16,
-                         B_PAIR = B_ABFULL + 17 /* [4] */, NBAR = B_ABFULL + 21;
+                         B_STAGED = B_ABFULL + 17 /* dq, dk, dv */, NBAR = B_ABFULL + 20;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int T0 = 0, T1 = 128, T2 = 256, T3 = 384;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-// v[c] of lane l, summed over the lanes: lane c gets the sum of v[c].
-__device__ __forceinline__ float column_sums(float (&v)[32]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) {
-        const bool up = (lane & s) != 0;
-#pragma unroll
-        for (int k = 0; k < s; ++k) {
-            const float keep = up ? v[k + s] : v[k], send = up ? v[k] : v[k + s];
-            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
-        }
-    }
-    return v[0];
-}
-
-// Scale 32 accumulator columns in place by f and return their dot product with
-// the row's 32 bf16 values in four chunks of a swizzled panel row.
-__device__ __forceinline__ float scale_dot32(uint32_t taddr, float f, uint32_t panel, int row, int chunk0) {
-    float x[32];
-    ld32f(taddr, x);
-    uint32_t w[32];
-    float dot = 0.f;
+// x . (the row's 32 bf16 values in four 16-byte pieces of a swizzled panel row).
+__device__ __forceinline__ float row_dot32(const float (&x)[32], uint32_t panel, int row, int chunk0) {
+    float d[2] = {0.f, 0.f};
 #pragma unroll
     for (int ch = 0; ch < 4; ++ch) {
         uint32_t a[4];
         ld_shared_v4(panel + sw128_off(row, chunk0 + ch), a[0], a[1], a[2], a[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int i = 8 * ch + 2 * e;
-            x[i] *= f;
-            x[i + 1] *= f;
-            dot = fmaf(x[i], bf16_lo(a[e]), dot);
-            dot = fmaf(x[i + 1], bf16_hi(a[e]), dot);
+            d[0] = fmaf(x[8 * ch + 2 * e], bf16_lo(a[e]), d[0]);
+            d[1] = fmaf(x[8 * ch + 2 * e + 1], bf16_hi(a[e]), d[1]);
         }
     }
+    return d[0] + d[1];
+}
+
+// Scale 32 accumulator columns in place.
+__device__ __forceinline__ void scale32(uint32_t taddr, float f, float (&x)[32]) {
+    uint32_t w[32];
+    ld32f(taddr, x);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(x[i]);
+    for (int i = 0; i < 32; ++i) {
+        x[i] *= f;
+        w[i] = __float_as_uint(x[i]);
+    }
     tmem_st32(taddr, w);
-    return dot;
+}
+
+// Start the TMA store of a staged [128][D] tile (one thread; its own bulk group).
+template <int D>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const uint8_t* tile, const GatedChunk& ch) {
+#pragma unroll
+    for (int pn = 0; pn < D / 64; ++pn) tma_store_3d(map, tile + pn * kPanel, pn * 64, ch.row, ch.group);
+    bulk_commit_group();
 }
 
 template <int D>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
     gated_grad_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_slots) {
     using Cfg = GrCfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -831,23 +941,21 @@ __global__ void __launch_bounds__(384, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.timeout_ns;
     const uint32_t sbase = smem_u32(smem);
-    // releases of K, Q and dO come from the warps that store dq, dk and dv out of them
-    constexpr int kStorers = Cfg::NPAN == 2 ? 8 : 4;
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::NS; ++s) {
             for (int t = 0; t < 6; ++t) {
                 mbar_init(&bar[Cfg::B_FULL + 6 * s + t], 1);
-                mbar_init(&bar[Cfg::B_EMPTY + 6 * s + t], t == Cfg::F_Q || t == Cfg::F_K || t == Cfg::F_O ? kStorers : 1);
+                // S and E are read by the products and by every warp
+                mbar_init(&bar[Cfg::B_EMPTY + 6 * s + t], t == Cfg::F_S || t == Cfg::F_E ? 17 : 1);
             }
             mbar_init(&bar[Cfg::B_GFULL + s], 1);
         }
-        for (int b : {Cfg::B_ABFULL, Cfg::B_X, Cfg::B_Y, Cfg::B_Z, Cfg::B_DQ, Cfg::B_DK, Cfg::B_DV, Cfg::B_SUMFREE,
+        for (int b : {Cfg::B_ABFULL, Cfg::B_Y, Cfg::B_Z, Cfg::B_DK, Cfg::B_DV, Cfg::B_SUMFREE,
                       Cfg::B_DONE})
             mbar_init(&bar[b], 1);
         for (int b : {Cfg::B_P, Cfg::B_XYS, Cfg::B_ZS, Cfg::B_FREE, Cfg::B_FREE + 1, Cfg::B_FREE + 2, Cfg::B_SUMS, Cfg::B_READ})
-            mbar_init(&bar[b], 8);
-        for (int b = 0; b < 4; ++b) mbar_init(&bar[Cfg::B_PAIR + b], 2);
+            mbar_init(&bar[b], 16);
+        for (int b = 0; b < 3; ++b) mbar_init(&bar[Cfg::B_STAGED + b], 4 * Cfg::NQ);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -880,7 +988,7 @@ __global__ void __launch_bounds__(384, 1)
                 const int s = static_cast<int>(g % Cfg::NS);
                 uint8_t* st = smem + s * Cfg::STAGE;
                 // in the order in which the tiles of the chunk before die
-                constexpr int order[6] = {Cfg::F_V, Cfg::F_E, Cfg::F_S, Cfg::F_K, Cfg::F_Q, Cfg::F_O};
+                constexpr int order[6] = {Cfg::F_V, Cfg::F_S, Cfg::F_E, Cfg::F_Q, Cfg::F_K, Cfg::F_O};
 #pragma unroll
                 for (int k = 0; k < 6; ++k) {
                     const int t = order[k];
@@ -934,7 +1042,7 @@ __global__ void __launch_bounds__(384, 1)
             auto wait = [&](int b, int64_t phase, unsigned where) {
                 return mbar_wait(&bar[b], static_cast<uint32_t>(phase & 1), abort_flag, tmo, where);
             };
-            walk([&](const GatedChunk&, int64_t, int64_t g) {
+            walk([&](const GatedChunk& ch, int64_t, int64_t g) {
                 const int s = static_cast<int>(g % Cfg::NS);
                 const int64_t k = g / Cfg::NS;
                 const uint32_t st = sbase + s * Cfg::STAGE;
@@ -943,6 +1051,8 @@ __global__ void __launch_bounds__(384, 1)
                 auto loaded = [&](int t) { return wait(Cfg::B_FULL + 6 * s + t, k, 0x810 + t); };
                 // T0, T1: scores (T0 and T1 of the chunk before are consumed and read)
                 if (!loaded(Cfg::F_Q) || !loaded(Cfg::F_K)) return false;
+                // the scores of a part-filled chunk need its zeroed rows
+                if (ch.nv < C && !wait(Cfg::B_GFULL + s, k, 0x817)) return false;
                 if (g >= 1 && (!wait(Cfg::B_DV, g - 1, 0x818) || !wait(Cfg::B_FREE + 2, g - 1, 0x819))) return false;
                 tc_fence_after();
                 issued = true;
@@ -965,7 +1075,7 @@ __global__ void __launch_bounds__(384, 1)
                 for (int ks = 0; ks < D / 16; ++ks)
                     mma_bf16_ss(tmem + Cfg::T2, sdesc_sw128(tile_k(o, ks, kPanel), 16, 1024),
                                 sdesc_sw128(tile_k(sb, ks, Cfg::SB_PANEL), 16, 1024), kIdS, ks > 0);
-                mma_commit(&bar[Cfg::B_X]);
+                mma_commit(empty(s, Cfg::F_S));
                 // T3 = V E^T
                 if (!loaded(Cfg::F_E)) return false;
                 if (g >= 1 && !wait(Cfg::B_FREE + 1, g - 1, 0x81b)) return false;
@@ -975,7 +1085,7 @@ __global__ void __launch_bounds__(384, 1)
                     mma_bf16_ss(tmem + Cfg::T3, sdesc_sw128(tile_k(v, ks, kPanel), 16, 1024),
                                 sdesc_sw128(tile_k(eb, ks, Cfg::SB_PANEL), 16, 1024), kIdS, ks > 0);
                 mma_commit(&bar[Cfg::B_Y]);
-                mma_commit(empty(s, Cfg::F_V));
+                if (D == 64) mma_commit(empty(s, Cfg::F_V));
                 // T1 = K E once the scores there are read
                 if (!wait(Cfg::B_P, g, 0x81c)) return false;
                 tc_fence_after();
@@ -992,8 +1102,7 @@ __global__ void __launch_bounds__(384, 1)
                 for (int ks = 0; ks < C / 16; ++ks)
                     mma_bf16_ss(tmem + Cfg::T2, sdesc_sw128(wt + ks * 2048, kPanel, 1024),
                                 sdesc_sw128(kk + ks * 2048, kPanel, 1024), kIdW, 1);
-                mma_commit(&bar[Cfg::B_DQ]);
-                mma_commit(empty(s, Cfg::F_S));
+                if (D == 128) mma_commit(empty(s, Cfg::F_V));
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks)
                     mma_bf16_ts(tmem + Cfg::T3, tmem + Cfg::T0 + 64 + ks * 8,
@@ -1024,34 +1133,59 @@ __global__ void __launch_bounds__(384, 1)
             scan_down(x, B, all);
             float R = __shfl_sync(0xffffffffu, G[3], ((lane >> 3) * 8 + 31) & 31);  // prefix before the block
             if (lane < 8) R = 0.f;
-            for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_O})
+            // (S: its last tile was given back behind the last use of these decays' place)
+            for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_V, Cfg::F_O, Cfg::F_S})
                 if (!mbar_wait_warp(full(s, t), ph, abort_flag, tmo, 0x820 + t)) return false;
-            // two sets of decays: the set's last readers, in chunk g - 2, were done before these tiles were loaded
             float4* o = reinterpret_cast<float4*>(smem + Cfg::OFF_G + (g & 1) * 4 * C * 4);
             o[lane] = make_float4(G[0], G[1], G[2], G[3]);
             o[32 + lane] = make_float4(ex2(G[0]), ex2(G[1]), ex2(G[2]), ex2(G[3]));
             o[64 + lane] = make_float4(ex2(B[0]), ex2(B[1]), ex2(B[2]), ex2(B[3]));
             o[96 + lane] = make_float4(ex2(G[0] - R), ex2(G[1] - R), ex2(G[2] - R), ex2(G[3] - R));
             if (ch.nv < C) {
-                for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_O}) zero_rows<D>(sbase + s * Cfg::STAGE + t * Cfg::TILE, ch.nv);
+                for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_V, Cfg::F_O})
+                    zero_rows<D>(sbase + s * Cfg::STAGE + t * Cfg::TILE, ch.nv);
                 fence_proxy_async_smem();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
+            // dv, the last result of the chunk
+            if (!mbar_wait_warp(&bar[Cfg::B_STAGED + 2], static_cast<uint32_t>(g & 1), abort_flag, tmo, 0x834)) return false;
+            if (lane == 0) {
+                if (ch.nv == C) {
+                    store_tile<D>(&m.dv, smem + s * Cfg::STAGE + Cfg::O, ch);
+                    bulk_wait_group_read<0>();
+                }
+                mbar_arrive(empty(s, Cfg::F_O));
+            }
+            __syncwarp();
             return true;
         });
+        if (lane == 0) bulk_wait_group<0>();
     } else if (warp == 3) {
         walk([&](const GatedChunk& ch, int64_t, int64_t g) {
-            if (!mbar_wait_warp(&bar[Cfg::B_SUMS], g & 1, abort_flag, tmo, 0x830)) return false;
-            const float4* rows = reinterpret_cast<const float4*>(smem + Cfg::OFF_ROWS);
-            const float4* cols = reinterpret_cast<const float4*>(smem + Cfg::OFF_COLS);
-            const float4* ri = reinterpret_cast<const float4*>(smem + Cfg::OFF_RI);
-            const float4* cj = reinterpret_cast<const float4*>(smem + Cfg::OFF_CJ);
+            const int s = static_cast<int>(g % Cfg::NS);
+            const uint32_t gp = static_cast<uint32_t>(g & 1);
+            auto store = [&](int n, int tile, const CUtensorMap* map) {
+                if (!mbar_wait_warp(&bar[Cfg::B_STAGED + n], gp, abort_flag, tmo, 0x832 + n)) return false;
+                if (lane == 0 && ch.nv == C) store_tile<D>(map, smem + s * Cfg::STAGE + tile * Cfg::TILE, ch);
+                return true;
+            };
+            if (!store(0, Cfg::F_Q, &m.dq) || !store(1, Cfg::F_K, &m.dk)) return false;
+            if (lane == 0) {  // hand each tile back as soon as its store has read it
+                if (ch.nv == C) bulk_wait_group_read<1>();
+                mbar_arrive(empty(s, Cfg::F_Q));
+                bulk_wait_group_read<0>();
+                mbar_arrive(empty(s, Cfg::F_K));
+            }
+            __syncwarp();
+            if (!mbar_wait_warp(&bar[Cfg::B_SUMS], gp, abort_flag, tmo, 0x830)) return false;
             const float* es = reinterpret_cast<const float*>(smem + Cfg::OFF_ES);
-            auto get = [&](const float4* a, int n, float (&x)[4]) {
+            auto get = [&](int off, float (&x)[4]) {
+                const float4* a = reinterpret_cast<const float4*>(smem + off);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = 0.f;
-                for (int k = 0; k < n; ++k) {
+#pragma unroll
+                for (int k = 0; k < Cfg::NQ; ++k) {
                     const float4 f = a[32 * k + lane];
                     x[0] += f.x;
                     x[1] += f.y;
@@ -1059,21 +1193,18 @@ __global__ void __launch_bounds__(384, 1)
                     x[3] += f.w;
                 }
             };
-            float r[4], c[4], u[4], d[4];
-            get(rows, (lane >> 3) + 1, r);  // blocks of keys up to the reader's own
-            get(cols, 2, c);
-            get(ri, 2, u);
-            get(cj, 2, d);
-            float e0 = 0.f;
+            float u[4], d[4], e0 = 0.f;
+            get(Cfg::OFF_U, u);
+            get(Cfg::OFF_CJ, d);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) e0 += es[k];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (4 * lane + e >= ch.nv) r[e] = c[e] = u[e] = d[e] = 0.f;
-                u[e] += r[e] - c[e];
-            }
+            for (int k = 0; k < 16; ++k) e0 += es[k];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_SUMFREE]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (4 * lane + e >= ch.nv) u[e] = d[e] = 0.f;
+                u[e] += d[e];
+            }
             float after[4], all, upto[4];
             scan_down(u, after, all);  // over i > t
             scan_up(d, upto);          // over j <= t
@@ -1085,15 +1216,14 @@ __global__ void __launch_bounds__(384, 1)
             }
             return true;
         });
+        if (lane == 0) bulk_wait_group<0>();
     } else {
-        const int sub = warp & 3, half = (warp - 4) >> 2, row = sub * 32 + lane;
-        constexpr int HC = D / 2;  // columns of this thread in the D-wide tiles
+        const int sub = warp & 3, quarter = (warp - 4) >> 2, row = sub * 32 + lane;
+        const bool wide = quarter < Cfg::NQ;  // has columns of the D-wide tiles
         const uint32_t lanes = static_cast<uint32_t>(sub * 32) << 16;
-        const uint32_t dcol = lanes + half * HC;
-        const int pan = D == 128 ? half : 0, ch0 = D == 128 ? 0 : 4 * half;  // this thread's panel and first 16-byte piece
-        float* rows = reinterpret_cast<float*>(smem + Cfg::OFF_ROWS);
-        float* cols = reinterpret_cast<float*>(smem + Cfg::OFF_COLS);
-        float* ri = reinterpret_cast<float*>(smem + Cfg::OFF_RI);
+        const uint32_t dcol = lanes + quarter * 32;
+        const int pan = quarter >> 1, ch0 = 4 * (quarter & 1);  // panel and first 16-byte piece of these columns
+        float* us = reinterpret_cast<float*>(smem + Cfg::OFF_U);
         float* cj = reinterpret_cast<float*>(smem + Cfg::OFF_CJ);
         float* es = reinterpret_cast<float*>(smem + Cfg::OFF_ES);
         walk([&](const GatedChunk& ch, int64_t, int64_t g) {
@@ -1110,16 +1240,106 @@ __global__ void __launch_bounds__(384, 1)
             if (!wait(Cfg::B_GFULL + s, ph, 0x840)) return false;
             const float* G = reinterpret_cast<const float*>(smem + Cfg::OFF_G + gp * 4 * C * 4);
             const float *Pre = G + C, *Suf = G + 2 * C, *F = G + 3 * C;
+            for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_S, Cfg::F_E})  // read here too
+                if (!wait(Cfg::B_FULL + 6 * s + t, ph, 0x842)) return false;
+            // decayed scores of key row j = row, readers i in block ib; warp-uniform cases
+            if (!wait(Cfg::B_ABFULL, gp, 0x844)) return false;
+            tc_fence_after();
+            const int ib = quarter;
+            uint32_t pw[16], ww[16];
+            if (ib < sub) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pw[e] = ww[e] = 0u;
+            } else {
+                const float Gj = G[row];
+                const uint32_t ta = tmem + Cfg::T0 + lanes + ib * 32, tb = tmem + Cfg::T1 + lanes + ib * 32;
+                if (ib > sub) {
+                    const float fj = ex2(G[ib * 32 - 1] - Gj);
+#pragma unroll
+                    for (int hb = 0; hb < 2; ++hb) {
+                        float a[16], b[16];
+                        ld16f(ta + hb * 16, a);
+                        ld16f(tb + hb * 16, b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 f = reinterpret_cast<const float4*>(F + ib * 32 + hb * 16)[e];
+                            const float w[4] = {fj * f.x, fj * f.y, fj * f.z, fj * f.w};
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int c = 4 * e + 2 * h;
+                                pw[8 * hb + 2 * e + h] = pack_bf16x2(w[2 * h] * a[c], w[2 * h + 1] * a[c + 1]);
+                                ww[8 * hb + 2 * e + h] = pack_bf16x2(w[2 * h] * b[c], w[2 * h + 1] * b[c + 1]);
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int hb = 0; hb < 2; ++hb) {
+                        float a[16], b[16];
+                        ld16f(ta + hb * 16, a);
+                        ld16f(tb + hb * 16, b);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float pv[2], wv[2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int c = 2 * e + h;
+                                const bool in = hb * 16 + c >= lane;
+                                const float w = ex2(G[ib * 32 + hb * 16 + c] - Gj);
+                                pv[h] = in ? w * a[c] : 0.f;
+                                wv[h] = in ? w * b[c] : 0.f;
+                            }
+                            pw[8 * hb + e] = pack_bf16x2(pv[0], pv[1]);
+                            ww[8 * hb + e] = pack_bf16x2(wv[0], wv[1]);
+                        }
+                    }
+                }
+            }
+            // every thread has read T0 and T1, and the products with V are done: the results take their place
+            tc_fence_before();
+            arrive(Cfg::B_READ);
+            if (!wait(Cfg::B_Y, gp, 0x846) || !wait(Cfg::B_READ, gp, 0x848)) return false;
+            tc_fence_after();
+            tmem_st16(tmem + Cfg::T0 + lanes + ib * 16, pw);
+            tmem_st16(tmem + Cfg::T0 + lanes + 64 + ib * 16, ww);
+            {
+                const uint32_t panel = sbase + Cfg::OFF_W + (ib >> 1) * kPanel;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    st_shared_v4(panel + sw128_off(row, 4 * (ib & 1) + c), ww[4 * c], ww[4 * c + 1], ww[4 * c + 2],
+                                 ww[4 * c + 3]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            fence_proxy_async_smem();
+            arrive(Cfg::B_P);
+            // scale the parts through the states (T2 before T3 was committed)
+            tc_fence_after();
             // the sums of the chunk before are read
             if (g >= 1 && !wait(Cfg::B_SUMFREE, gp ^ 1u, 0x841)) return false;
-            // e^{G_C} <E, S>, a share of rows per thread
-            if (!wait(Cfg::B_FULL + 6 * s + Cfg::F_S, ph, 0x842) || !wait(Cfg::B_FULL + 6 * s + Cfg::F_E, ph, 0x843))
-                return false;
+            if (wide) {
+                float x[32];
+                scale32(tmem + Cfg::T2 + dcol, Pre[row], x);
+                scale32(tmem + Cfg::T3 + dcol, Suf[row], x);
+                cj[quarter * C + row] = row_dot32(x, st + Cfg::K + pan * kPanel, row, ch0);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(Cfg::B_XYS);
+            if (!wait(Cfg::B_Z, gp, 0x847)) return false;
+            tc_fence_after();
+            if (wide) {
+                float x[32];
+                scale32(tmem + Cfg::T1 + dcol, Suf[row], x);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(Cfg::B_ZS);
+            // e^{G_C} <E, S>, a share of the elements per thread
             {
                 float acc = 0.f;
-                const int t = threadIdx.x - 128;
 #pragma unroll 2
-                for (int i = t * 16; i < Cfg::SB; i += 256 * 16) {
+                for (int i = (threadIdx.x - 128) * 16; i < Cfg::SB; i += 512 * 16) {
                     uint32_t a[4], b[4];
                     ld_shared_v4(st + Cfg::S + i, a[0], a[1], a[2], a[3]);
                     ld_shared_v4(st + Cfg::E + i, b[0], b[1], b[2], b[3]);
@@ -1131,140 +1351,47 @@ __global__ void __launch_bounds__(384, 1)
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-                if (lane == 0) es[warp - 4] = Pre[C - 1] * acc;
-            }
-            // decayed scores of key row j = row, readers i in this half
-            if (!wait(Cfg::B_ABFULL, gp, 0x844)) return false;
-            tc_fence_after();
-            uint32_t pw[32], ww[32];
-            float csum = 0.f;
-            const float Gj = G[row];
-#pragma unroll
-            for (int qd = 0; qd < 2; ++qd) {
-                const int ib = 2 * half + qd;  // block of 32 readers; warp-uniform cases
-                if (ib < sub) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pw[16 * qd + e] = ww[16 * qd + e] = 0u;
-                    continue;
+                if (lane == 0) {
+                    es[warp - 4] = Pre[C - 1] * acc;
+                    mbar_arrive(empty(s, Cfg::F_S));
+                    mbar_arrive(empty(s, Cfg::F_E));
                 }
-                float a[32], b[32];
-                ld32f(tmem + Cfg::T0 + lanes + ib * 32, a);
-                ld32f(tmem + Cfg::T1 + lanes + ib * 32, b);
-                const float fj = ib > sub ? ex2(G[ib * 32 - 1] - Gj) : 0.f;
-                const bool rowin = row < ch.nv;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float w[2], pv[2], wv[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int i = ib * 32 + 2 * e + h;
-                        const bool in = rowin && i < ch.nv && i >= row;
-                        w[h] = ib > sub ? fj * F[i] : ex2(G[i] - Gj);
-                        pv[h] = in ? w[h] * a[2 * e + h] : 0.f;
-                        wv[h] = in ? w[h] * b[2 * e + h] : 0.f;
-                        a[2 * e + h] = in && i > row ? pv[h] * b[2 * e + h] : 0.f;  // M
-                        csum += a[2 * e + h];
-                    }
-                    pw[16 * qd + e] = pack_bf16x2(pv[0], pv[1]);
-                    ww[16 * qd + e] = pack_bf16x2(wv[0], wv[1]);
-                }
-                const float rs = column_sums(a);
-                rows[sub * C + ib * 32 + lane] = rs;
             }
-            cols[half * C + row] = csum;
-            // every thread has read T0, T1 and S, whose place the results take
-            tc_fence_before();
-            arrive(Cfg::B_READ);
-            if (!wait(Cfg::B_X, gp, 0x845) || !wait(Cfg::B_READ, gp, 0x848)) return false;
-            tc_fence_after();
-            tmem_st32(tmem + Cfg::T0 + lanes + half * 32, pw);
-            tmem_st32(tmem + Cfg::T0 + lanes + 64 + half * 32, ww);
-            {
-                const uint32_t panel = sbase + Cfg::OFF_W + half * kPanel;
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    st_shared_v4(panel + sw128_off(row, c), ww[4 * c], ww[4 * c + 1], ww[4 * c + 2], ww[4 * c + 3]);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            fence_proxy_async_smem();
-            arrive(Cfg::B_P);
-            // scale the parts through the states, with their terms of dg
-            tc_fence_after();
-            float dot = 0.f;
-#pragma unroll
-            for (int h = 0; h < HC / 32; ++h)
-                dot += scale_dot32(tmem + Cfg::T2 + dcol + h * 32, Pre[row], st + Cfg::Q + pan * kPanel, row, ch0 + 4 * h);
-            ri[half * C + row] = dot;
-            if (!wait(Cfg::B_Y, gp, 0x846)) return false;
-            tc_fence_after();
-            dot = 0.f;
-#pragma unroll
-            for (int h = 0; h < HC / 32; ++h)
-                dot += scale_dot32(tmem + Cfg::T3 + dcol + h * 32, Suf[row], st + Cfg::K + pan * kPanel, row, ch0 + 4 * h);
-            cj[half * C + row] = dot;
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(Cfg::B_XYS);
-            arrive(Cfg::B_SUMS);
-            if (!wait(Cfg::B_Z, gp, 0x847)) return false;
-            tc_fence_after();
-#pragma unroll
-            for (int h = 0; h < HC / 32; ++h) {
-                float x[32];
-                ld32f(tmem + Cfg::T1 + dcol + h * 32, x);
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(x[e] * Suf[row]);
-                tmem_st32(tmem + Cfg::T1 + dcol + h * 32, w);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(Cfg::B_ZS);
-            // results
-            auto result = [&](int ready, int tm, int freed, int tile, const CUtensorMap* map, void* dst) -> bool {
-                if (!wait(ready, gp, 0x850 + tile)) return false;
-                tc_fence_after();
-                const uint32_t panel = st + tile * Cfg::TILE + pan * kPanel;
-                uint16_t* out = static_cast<uint16_t*>(dst) + (ch.row0 + row) * D + half * HC;
-#pragma unroll
-                for (int h = 0; h < HC / 32; ++h) {
+            // results: into the tile of q, k or dO, whose last reader is done
+            auto result = [&](int tm, int n, int tile, void* dst, bool dot) -> float {
+                float sum = 0.f;
+                if (wide) {
+                    const uint32_t panel = st + tile * Cfg::TILE + pan * kPanel;
                     float x[32];
-                    ld32f(tmem + tm + dcol + h * 32, x);
+                    ld32f(tmem + tm + dcol, x);
+                    if (dot) sum = row_dot32(x, panel, row, ch0);
                     if (ch.nv == C) {
-                        put_row32(panel, row, ch0 + 4 * h, x);
+                        put_row32(panel, row, ch0, x);
+                        fence_proxy_async_smem();
                     } else if (row < ch.nv) {
+                        uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + (ch.row0 + row) * D + quarter * 32);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<uint4*>(out + h * 32)[e] = make_uint4(
-                                pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
-                                pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
+                            out[e] = make_uint4(pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
+                                                pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
                     }
                 }
                 tc_fence_before();
-                fence_proxy_async_smem();
-                arrive(Cfg::B_FREE + freed);
-                if (D == 64) {  // two warps fill a panel's 32 rows (three results a chunk)
-                    arrive(Cfg::B_PAIR + sub);
-                    if (!wait(Cfg::B_PAIR + sub, static_cast<uint32_t>((3 * g + freed) & 1), 0x849)) return false;
-                }
-                if (lane == 0 && (D == 128 || half == 0)) {
-                    if (ch.nv == C) {
-                        tma_store_3d(map, smem + s * Cfg::STAGE + tile * Cfg::TILE + pan * kPanel + sub * 32 * 128,
-                                     pan * 64, ch.row + sub * 32, ch.group);
-                        bulk_commit_group();
-                        bulk_wait_group_read<0>();
-                    }
-                    mbar_arrive(empty(s, tile));
-                }
-                __syncwarp();
-                return true;
+                arrive(Cfg::B_FREE + n);
+                if (wide && lane == 0) mbar_arrive(&bar[Cfg::B_STAGED + n]);
+                return sum;
             };
-            return result(Cfg::B_DQ, Cfg::T2, 0, Cfg::F_K, &m.dq, p.dq) &&
-                   result(Cfg::B_DK, Cfg::T3, 1, Cfg::F_Q, &m.dk, p.dk_) &&
-                   result(Cfg::B_DV, Cfg::T1, 2, Cfg::F_O, &m.dv, p.dv_);
+            if (!wait(Cfg::B_DK, gp, 0x850)) return false;
+            tc_fence_after();
+            float u = result(Cfg::T2, 0, Cfg::F_Q, p.dq, true);
+            u -= result(Cfg::T3, 1, Cfg::F_K, p.dk_, true);
+            if (wide) us[quarter * C + row] = u;
+            arrive(Cfg::B_SUMS);
+            if (!wait(Cfg::B_DV, gp, 0x851)) return false;
+            tc_fence_after();
+            result(Cfg::T1, 2, Cfg::F_O, p.dv_, false);
+            return true;
         });
-        if (lane == 0) bulk_wait_group<0>();
     }
 
     tc_fence_before();

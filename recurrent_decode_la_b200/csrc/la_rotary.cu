@@ -22,6 +22,7 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
@@ -90,21 +91,30 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryProblem p,
         const T* x = static_cast<const T*>(p.x[which]);
         T* y = static_cast<T*>(p.y[which]);
         if (x == nullptr) continue;
-#pragma unroll 4
-        for (int64_t h = 0; h < h1 - h0; ++h) {
-            Vec<T, V> u = *reinterpret_cast<const Vec<T, V>*>(x + a0 + h * step);
-            Vec<T, V> w = *reinterpret_cast<const Vec<T, V>*>(x + a1 + h * step);
+        // kBatch heads are loaded before the first is stored (the output may be the input)
+        for (int64_t hb = 0; hb < h1 - h0; hb += kBatch) {
+            Vec<T, V> u[kBatch], w[kBatch];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                // the pair's elements: (u[e], w[e]), or, interleaved, entries 2e and 2e + 1 of u followed by w
-                T& ra = INTERLEAVED ? (2 * e < V ? u.x[(2 * e) % V] : w.x[(2 * e) % V]) : u.x[e];
-                T& rb = INTERLEAVED ? (2 * e + 1 < V ? u.x[(2 * e + 1) % V] : w.x[(2 * e + 1) % V]) : w.x[e];
-                const float fa = get(ra), fb = get(rb);
-                put(ra, fa * c[e] - fb * s[e]);
-                put(rb, fb * c[e] + fa * s[e]);
+            for (int n = 0; n < kBatch; ++n)
+                if (hb + n < h1 - h0) {
+                    u[n] = *reinterpret_cast<const Vec<T, V>*>(x + a0 + (hb + n) * step);
+                    w[n] = *reinterpret_cast<const Vec<T, V>*>(x + a1 + (hb + n) * step);
+                }
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) {
+                if (hb + n >= h1 - h0) break;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    // the pair's elements: (u[e], w[e]), or, interleaved, entries 2e and 2e + 1 of u followed by w
+                    T& ra = INTERLEAVED ? (2 * e < V ? u[n].x[(2 * e) % V] : w[n].x[(2 * e) % V]) : u[n].x[e];
+                    T& rb = INTERLEAVED ? (2 * e + 1 < V ? u[n].x[(2 * e + 1) % V] : w[n].x[(2 * e + 1) % V]) : w[n].x[e];
+                    const float fa = get(ra), fb = get(rb);
+                    put(ra, fa * c[e] - fb * s[e]);
+                    put(rb, fb * c[e] + fa * s[e]);
+                }
+                *reinterpret_cast<Vec<T, V>*>(y + a0 + (hb + n) * step) = u[n];
+                *reinterpret_cast<Vec<T, V>*>(y + a1 + (hb + n) * step) = w[n];
             }
-            *reinterpret_cast<Vec<T, V>*>(y + a0 + h * step) = u;
-            *reinterpret_cast<Vec<T, V>*>(y + a1 + h * step) = w;
         }
     }
 }

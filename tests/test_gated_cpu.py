@@ -193,9 +193,34 @@ def test_binding_refusals():
     bad(la.la_rotary_init, z(2, 2))
 
 
-def test_binding_refuses_two_devices():
+def test_binding_argument_checks():
+    """Each property that the ordinary call's one test covers is refused by itself."""
     from recurrent_decode_la_b200 import binding
-    a, b = torch.zeros(1), torch.zeros(1, device="meta")
+
+    class Fake:
+        dtype, shape, device, is_cuda, dev, contiguous = torch.float32, torch.Size((2, 3)), "cuda:1", True, 1, True
+
+        def __init__(self, **kw):
+            self.__dict__.update(kw)
+
+        def get_device(self):
+            return self.dev
+
+        def is_contiguous(self):
+            return self.contiguous
+
+        def data_ptr(self):
+            return 4096
+
+        def numel(self):
+            return 6
+
+    def check(t):
+        return binding._arg(t, "x", (2, 3), torch.float32, 1)
+
+    assert check(Fake()) == 4096
+    for bad in (dict(dtype=torch.bfloat16), dict(shape=torch.Size((3, 2))), dict(dev=0), dict(dev=-1, is_cuda=False), dict(contiguous=False)):
+        with pytest.raises(ValueError):
+            check(Fake(**bad))
     with pytest.raises(ValueError):
-        binding._one_device(q=a, k=b)
-    assert binding._one_device(q=a, k=None, v=a) == a.device
+        binding._floats(Fake(), "x", 7, 1)

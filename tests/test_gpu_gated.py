@@ -155,6 +155,22 @@ def test_long_and_few_units(dtype, dk, dv):
     check_backward(x, dtype, s0=False)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,T,lens", [(2, 16, 4096, None), (1, 24, 6000, None), (1, 16, 5555, [3000, 1, 0, 700, 129, 1725])])
+def test_many_chunks(d, B, H, T, lens):
+    """More chunks than the device holds at once, each compared by itself with the float32 kernels on the same values,
+    twice: a chunk that went wrong through its neighbour's tiles shows in one of them."""
+    x = make(23, BF16, B, H, T, d, d, "mild", lens)
+    y = {m: t.float() if isinstance(t, torch.Tensor) and t.dtype == BF16 else t for m, t in x.items()}
+    want = [*run_prefill(y)[:1], *run_backward(y)[:4]]
+    for _ in range(2):
+        got = [*run_prefill(x)[:1], *run_backward(x)[:4]]
+        for name, a, b in zip(("o", "dq", "dk", "dv", "dg"), got, want):
+            a, b = (t.double().reshape(H * B, T, -1)[:, :T // 128 * 128].reshape(H * B, T // 128, -1) for t in (a, b))
+            err = (a - b).norm(dim=-1) / b.norm(dim=-1).clamp_min(float(b.norm()) / b.shape[1] ** 0.5 / (H * B) ** 0.5 / 4)
+            assert bool((err <= 2 * TOL[BF16]).all()), (name, float(err.max()), int((err > 2 * TOL[BF16]).sum()))
+
+
 def test_no_decay_is_the_plain_prefill():
     x = make(3, BF16, 2, 4, 500, 128, 128, None)
     o, S = run_prefill(x)
