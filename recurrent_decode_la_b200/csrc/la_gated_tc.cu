@@ -356,18 +356,17 @@ __global__ void __launch_bounds__(640, 1)
             const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE;
             const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + Cfg::OFF_W + (g % Cfg::NW) * 3 * C * 2);
             // w x = hi + mid + lo for two values at a time, in paired bf16 arithmetic.  A product of two 8-bit
-            // significands has 16 bits, so w0 x = hi + r and w1 x = p + e1 exactly; r + p = mid + e2 exactly; what
-            // follows is rounded, 2^-26 of w x.
+            // significands has 16 bits, so w0 x = hi + r exactly; mid = r + p with p = w1 x rounded, and m - r is
+            // exact, so w1 x - (m - r) is what both roundings lost.  A state is 1e-7 of itself off; 2.4e-6 where lo
+            // takes only (w1 + w2) x, which saves three operations and 5 % of the time.
             auto split = [](uint32_t x2, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
                 auto b = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
                 auto u = [](__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); };
                 const __nv_bfloat162 x = b(x2), h = __hmul2_rn(b(w0), x), r = __hfma2(b(w0), x, __hneg2(h)),
-                                     p = __hmul2_rn(b(w1), x), e1 = __hfma2(b(w1), x, __hneg2(p)), m = __hadd2_rn(r, p),
-                                     q = __hsub2_rn(m, r),
-                                     e2 = __hadd2_rn(__hsub2_rn(r, __hsub2_rn(m, q)), __hsub2_rn(p, q));
+                                     m = __hadd2_rn(r, __hmul2_rn(b(w1), x)), q = __hsub2_rn(m, r);
                 hi = u(h);
                 mid = u(m);
-                lo = u(__hfma2(b(w2), x, __hadd2_rn(e1, e2)));
+                lo = u(__hfma2(b(w2), x, __hfma2(b(w1), x, __hneg2(q))));
             };
             const bool lofree = g < Cfg::NL;
             const uint32_t loph = ((g / Cfg::NL) + 1) & 1;
@@ -377,34 +376,46 @@ __global__ void __launch_bounds__(640, 1)
                 if (nv < C)
                     for (int row = nv + (warp - 4); row < C; row += 8)
                         if (lane < 16) st_shared_v4(y + (lane >> 3) * kPanel + row * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+                if (!lofree && !mbar_wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
+                    return false;
+                tc_fence_after();
+                const uint32_t tp = tmem + Cfg::tm_part(g % Cfg::NL, 0) + half * 32 + (static_cast<uint32_t>(sub * 32) << 16);
 #pragma unroll
-                for (int grp = 0; grp < 2; ++grp) {
-                    uint32_t part[3][16];
-                    const int c0 = 4 * sub + 2 * grp;  // first 16-byte piece of the 16 columns
-                    const uint32_t panel = x + (c0 >> 3) * kPanel;
-                    const int tok = 64 * half + (lane & 7) + ((lane >> 4) << 3), ch = (c0 & 7) + ((lane >> 3) & 1);
+                for (int kk = 0; kk < 4; kk += 2) {  // 32 tokens
+                    uint32_t part[2][3][8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t a[4];
-                        ldmatrix_x4_trans(panel + sw128_off(tok + 16 * k, ch), a[0], a[1], a[2], a[3]);
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t wr[2][3];  // decays of token pairs t0, t0 + 1 and t0 + 8, t0 + 9
+                        const int t0 = 64 * half + 16 * (kk + k) + 2 * (lane & 3);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int t0 = 64 * half + 16 * k + 8 * (r >> 1) + 2 * (lane & 3);
-                            uint32_t v = a[r];
-                            if (nv < C) v &= (t0 < nv ? 0xffffu : 0u) | (t0 + 1 < nv ? 0xffff0000u : 0u);
-                            split(v, w[t0 >> 1], w[64 + (t0 >> 1)], w[128 + (t0 >> 1)], part[0][4 * k + r], part[1][4 * k + r], part[2][4 * k + r]);
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll
+                            for (int e = 0; e < 3; ++e) wr[r][e] = w[64 * e + (t0 >> 1) + 4 * r];
+#pragma unroll
+                        for (int grp = 0; grp < 2; ++grp) {
+                            const int c0 = 4 * sub + 2 * grp;  // first 16-byte piece of the 16 columns
+                            const int tok = 64 * half + 16 * (kk + k) + (lane & 7) + ((lane >> 4) << 3),
+                                      ch = (c0 & 7) + ((lane >> 3) & 1);
+                            uint32_t a[4];
+                            ldmatrix_x4_trans(x + (c0 >> 3) * kPanel + sw128_off(tok, ch), a[0], a[1], a[2], a[3]);
+                            if (nv < C) {
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) {
+                                    const int t = t0 + 8 * (r >> 1);
+                                    a[r] &= (t < nv ? 0xffffu : 0u) | (t + 1 < nv ? 0xffff0000u : 0u);
+                                }
+                            }
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                split(a[r], wr[r >> 1][0], wr[r >> 1][1], wr[r >> 1][2], part[grp][0][4 * k + r],
+                                      part[grp][1][4 * k + r], part[grp][2][4 * k + r]);
                         }
                     }
-                    if (grp == 0) {
-                        if (!lofree && !mbar_wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
-                            return false;
-                        tc_fence_after();
-                    }
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        tmem_st_16x128b_x8(tmem + Cfg::tm_part(g % Cfg::NL, k) + half * 32 +
-                                               (static_cast<uint32_t>(sub * 32 + grp * 16) << 16),
-                                           part[k]);
+                    for (int grp = 0; grp < 2; ++grp)
+#pragma unroll
+                        for (int e = 0; e < 3; ++e)
+                            tmem_st_16x128b_x4(tp + e * 64 + kk * 8 + (static_cast<uint32_t>(grp * 16) << 16), part[grp][e]);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1133,9 +1144,10 @@ __global__ void __launch_bounds__(640, 1)
             scan_down(x, B, all);
             float R = __shfl_sync(0xffffffffu, G[3], ((lane >> 3) * 8 + 31) & 31);  // prefix before the block
             if (lane < 8) R = 0.f;
-            // (S: its last tile was given back behind the last use of these decays' place)
-            for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_V, Cfg::F_O, Cfg::F_S})
-                if (!mbar_wait_warp(full(s, t), ph, abort_flag, tmo, 0x820 + t)) return false;
+            // (S: its tile was given back behind the last use of these decays' place.  V is waited for only where its
+            // rows are zeroed: a full chunk's V may be given back, and loaded again, before this warp looks at it)
+            for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_O, Cfg::F_S, Cfg::F_V})
+                if ((t != Cfg::F_V || ch.nv < C) && !mbar_wait_warp(full(s, t), ph, abort_flag, tmo, 0x820 + t)) return false;
             float4* o = reinterpret_cast<float4*>(smem + Cfg::OFF_G + (g & 1) * 4 * C * 4);
             o[lane] = make_float4(G[0], G[1], G[2], G[3]);
             o[32 + lane] = make_float4(ex2(G[0]), ex2(G[1]), ex2(G[2]), ex2(G[3]));
