@@ -58,6 +58,7 @@ struct GatedProblem {
     int dv;
     const int32_t* cu;     // nullptr: dense
     const int32_t* choff;  // packed: chunks before sequence n, num_seqs + 1 entries
+    const int32_t* order;  // packed: the sequences, longest first (nullptr: in their order)
     int64_t nc;            // chunk slots per group
     void* s_states;        // state at each chunk's start
     void* e_states;        // gradient of the state at each chunk's end
@@ -115,8 +116,11 @@ __device__ __forceinline__ GatedChunk gated_chunk(const GatedProblem& p, int64_t
 }
 
 // choff[n] = chunks of C tokens in the sequences before n (offsets out of
-// range or decreasing: an empty sequence), n = 0 .. num_seqs.
-cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, int C, int32_t* choff,
+// range or decreasing: an empty sequence), n = 0 .. num_seqs.  order (may be
+// nullptr): the sequences by decreasing chunks, ties by index, for at most
+// kMaxGatedOrder of them.
+constexpr int kMaxGatedOrder = 1024;
+cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, int C, int32_t* choff, int32_t* order,
                                  cudaStream_t s);
 
 // CUDA-core kernels: fp32 throughout, fp32 chunk states, any d_k, d_v <= 128.

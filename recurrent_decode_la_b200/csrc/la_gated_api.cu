@@ -29,7 +29,7 @@ Kernel choose(la_dtype dtype, int64_t max_tokens, int dk, int dv, bool grad) {
 }
 
 // Chunk states in the workspace: packed, first the chunk offsets (num_seqs + 1
-// int32); then one state per chunk slot, and for the gradient one gradient of
+// int32) and the sequences by length (num_seqs int32); then one state per chunk slot, and for the gradient one gradient of
 // a state per slot.
 struct Layout {
     int chunk = 0;
@@ -43,7 +43,7 @@ Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs
     // a packed sequence begins a chunk of its own
     w.nc = num_seqs > 0 ? T / w.chunk + num_seqs : (T + w.chunk - 1) / w.chunk;
     const size_t states = up256(static_cast<size_t>(groups) * w.nc * dk * dv * (kind == kTc ? 2 : 4));
-    w.s = num_seqs > 0 ? up256((static_cast<size_t>(num_seqs) + 1) * 4) : 0;
+    w.s = num_seqs > 0 ? up256((2 * static_cast<size_t>(num_seqs) + 1) * 4) : 0;
     w.e = w.s + states;
     w.bytes = w.e + (grad ? states : 0);
     return w;
@@ -92,6 +92,7 @@ la_status place(GatedProblem& p, const Layout& w, void* workspace, size_t bytes)
     char* base = static_cast<char*>(workspace);
     p.nc = w.nc;
     p.choff = p.cu ? reinterpret_cast<const int32_t*>(base) : nullptr;
+    p.order = p.cu && p.num_seqs <= kMaxGatedOrder ? p.choff + p.num_seqs + 1 : nullptr;
     p.s_states = base + w.s;
     p.e_states = base + w.e;
     return LA_OK;
@@ -99,7 +100,7 @@ la_status place(GatedProblem& p, const Layout& w, void* workspace, size_t bytes)
 
 cudaError_t chunk_offsets(const GatedProblem& p, const Layout& w, cudaStream_t s) {
     if (!p.cu) return cudaSuccess;
-    return launch_chunk_offsets(p.cu, p.num_seqs, p.rows, w.chunk, const_cast<int32_t*>(p.choff), s);
+    return launch_chunk_offsets(p.cu, p.num_seqs, p.rows, w.chunk, const_cast<int32_t*>(p.choff), const_cast<int32_t*>(p.order), s);
 }
 
 // The tensor maps of the tensor-core kernels (every tensor 16-byte aligned).

@@ -395,8 +395,9 @@ __global__ void __launch_bounds__(kThreads) gated_grad_simt_kernel(const GatedPr
 }
 
 __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __restrict__ cu, int num_seqs, int64_t rows,
-                                                             int chunk, int32_t* __restrict__ choff) {
+                                                             int chunk, int32_t* __restrict__ choff, int32_t* __restrict__ order) {
     __shared__ int64_t warp_sum[32];
+    __shared__ int32_t chunks[kMaxGatedOrder];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     int64_t before = 0;
     for (int n0 = 0; n0 < num_seqs; n0 += 1024) {
@@ -405,6 +406,7 @@ __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __re
         if (n < num_seqs) {
             const int a = cu[n], b = cu[n + 1];
             if (!(a < 0 || b < a || static_cast<int64_t>(b) > rows)) x = (b - a + chunk - 1) / chunk;
+            if (order != nullptr) chunks[n] = x;
         }
         int64_t s = x;
         for (int o = 1; o < 32; o <<= 1) {
@@ -423,6 +425,12 @@ __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __re
         __syncthreads();
     }
     if (tid == 0) choff[num_seqs] = static_cast<int32_t>(min(before, static_cast<int64_t>(0x7fffffff)));
+    if (order != nullptr && tid < num_seqs) {  // the rank: how many sort before this one
+        const int32_t x = chunks[tid];
+        int rank = 0;
+        for (int n = 0; n < num_seqs; ++n) rank += chunks[n] > x || (chunks[n] == x && n < tid) ? 1 : 0;
+        order[rank] = tid;
+    }
 }
 
 template <typename F>
@@ -465,8 +473,9 @@ cudaError_t grad_t(const GatedProblem& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, int chunk, int32_t* choff,
-                                 cudaStream_t s) {
-    chunk_offsets_kernel<<<1, 1024, 0, s>>>(cu, num_seqs, rows, chunk, choff);
+                                 int32_t* order, cudaStream_t s) {
+    if (num_seqs > kMaxGatedOrder) order = nullptr;
+    chunk_offsets_kernel<<<1, 1024, 0, s>>>(cu, num_seqs, rows, chunk, choff, order);
     return cudaGetLastError();
 }
 

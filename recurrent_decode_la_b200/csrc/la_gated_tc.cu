@@ -140,8 +140,10 @@ __device__ __forceinline__ uint32_t tile_k(uint32_t tile, int ks, uint32_t panel
 }
 
 // ---------------------------------------------------------------------------
-// States.  Work item i < n_units: unit i forward, X = K, Y = V; the others
-// (gradient): unit i - n_units in reverse, X = Q, Y = dO.  Per chunk
+// States.  A work item is a unit, forward: X = K, Y = V; for the gradient also
+// in reverse: X = Q, Y = dO.  The units of packed input come longest first
+// (p.order), dealt to the CTAs in turn and back, so that no CTA gets the longer
+// item of every round.  Per chunk
 //     U = X'^T Y (X' = the decayed rows, as the sum of three bf16 numbers),
 //     S = gamma S + U.
 //   warp 0       TMA producer        warp 1  MMA issuer
@@ -183,7 +185,7 @@ struct StCfg {
 
 template <int D>
 __global__ void __launch_bounds__(640, 1)
-    gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items) {
+    gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items, bool grad) {
     using Cfg = StCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -221,19 +223,28 @@ __global__ void __launch_bounds__(640, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // Calls f(unit, chunk, rows of it, global chunk number) for every chunk of this CTA's items, until f gives up.
+    // Calls f(unit, its state, reverse) for every item of this CTA until f gives up.
+    auto items = [&](auto&& f) {
+        for (int64_t k = 0;; ++k) {
+            const int64_t i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (k * gridDim.x >= n_items) return true;
+            if (i >= n_items) continue;
+            int64_t u = grad ? i >> 1 : i;
+            if (p.order != nullptr) u = static_cast<int64_t>(p.order[u / p.H]) * p.H + u % p.H;
+            if (!f(gated_unit(p, u), u, grad && (i & 1))) return false;
+        }
+    };
+    // Calls f(unit, reverse, chunk, rows of it, chunks before it) for every chunk of them.
     auto walk = [&](auto&& f) -> bool {
         int64_t g = 0;
-        for (int64_t i = blockIdx.x; i < n_items; i += gridDim.x) {
-            const bool rev = i >= p.n_units;
-            const GatedUnit un = gated_unit(p, rev ? i - p.n_units : i);
+        return items([&](const GatedUnit& un, int64_t, bool rev) {
             const int nch = (un.len + C - 1) / C;
             for (int cc = 0; cc < nch; ++cc, ++g) {
                 const int c = rev ? nch - 1 - cc : cc;
                 if (!f(un, rev, c, min(C, un.len - c * C), g)) return false;
             }
-        }
-        return true;
+            return true;
+        });
     };
 
     if (warp == 0) {
@@ -461,13 +472,9 @@ __global__ void __launch_bounds__(640, 1)
         constexpr int kRows = D / 4;  // rows of this warp
         float S[64];
         int64_t g = 0;
-        bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-            const bool rev = i >= p.n_units;
-            const int64_t u = rev ? i - p.n_units : i;
-            const GatedUnit un = gated_unit(p, u);
+        items([&](const GatedUnit& un, int64_t u, bool rev) {
             const int nch = (un.len + C - 1) / C;
-            if (nch == 0) continue;
+            if (nch == 0) return true;
             const float* in = rev ? p.dstate : (p.state ? p.state : p.s0);
             float* out = rev ? p.dstate : p.state;
             const int64_t at = u * D * D + static_cast<int64_t>(row < 0 ? 0 : row) * D + half * 64;
@@ -501,10 +508,7 @@ __global__ void __launch_bounds__(640, 1)
                     bulk_store(slots + static_cast<int64_t>(c) * Cfg::SB + off, smem + Cfg::OFF_SB + off, kRows * 128);
                     bulk_commit_group();
                 }
-                if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) {
-                    ok = false;
-                    break;
-                }
+                if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) return false;
                 tc_fence_after();
                 const float gamma = gam[g % Cfg::kGam];
 #pragma unroll
@@ -518,13 +522,14 @@ __global__ void __launch_bounds__(640, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[Cfg::B_UEMPTY + b]);
             }
-            if (ok && out && row >= 0) {
+            if (out && row >= 0) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     reinterpret_cast<float4*>(out + at)[j] =
                         make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
             }
-        }
+            return true;
+        });
         if (lane == 0) bulk_wait_group<0>();
     }
 
@@ -1426,7 +1431,7 @@ cudaError_t states_d(const GatedProblem& p, const GatedMaps& m, bool grad, int n
     cudaError_t e = raise_smem(once, gated_states_tc_kernel<D>, StCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t items = grad ? 2 * p.n_units : p.n_units;
-    gated_states_tc_kernel<D><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items);
+    gated_states_tc_kernel<D><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items, grad);
     return cudaGetLastError();
 }
 template <int D>
