@@ -135,6 +135,33 @@ __device__ __forceinline__ void ld16f(uint32_t taddr, float (&x)[16]) {
     }
 }
 
+// Two loads in flight, one wait.
+__device__ __forceinline__ void ld16f2(uint32_t ta, uint32_t tb, float (&x)[16], float (&y)[16]) {
+    uint32_t r[16], q[16];
+    tmem_ld16(ta, r);
+    tmem_ld16(tb, q);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        asm volatile("" : "+r"(r[i]), "+r"(q[i]));
+        x[i] = __uint_as_float(r[i]);
+        y[i] = __uint_as_float(q[i]);
+    }
+}
+
+__device__ __forceinline__ void ld32f2(uint32_t ta, uint32_t tb, float (&x)[32], float (&y)[32]) {
+    uint32_t r[32], q[32];
+    tmem_ld32(ta, r);
+    tmem_ld32(tb, q);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        asm volatile("" : "+r"(r[i]), "+r"(q[i]));
+        x[i] = __uint_as_float(r[i]);
+        y[i] = __uint_as_float(q[i]);
+    }
+}
+
 __device__ __forceinline__ uint32_t tile_k(uint32_t tile, int ks, uint32_t panel) {  // K-major step ks
     return tile + (ks >> 2) * panel + (ks & 3) * 32;
 }
@@ -910,28 +937,30 @@ struct GrCfg {
 
 // x . (the row's 32 bf16 values in four 16-byte pieces of a swizzled panel row).
 __device__ __forceinline__ float row_dot32(const float (&x)[32], uint32_t panel, int row, int chunk0) {
-    float d[2] = {0.f, 0.f};
+    float2 d[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int ch = 0; ch < 4; ++ch) {
         uint32_t a[4];
         ld_shared_v4(panel + sw128_off(row, chunk0 + ch), a[0], a[1], a[2], a[3]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            d[0] = fmaf(x[8 * ch + 2 * e], bf16_lo(a[e]), d[0]);
-            d[1] = fmaf(x[8 * ch + 2 * e + 1], bf16_hi(a[e]), d[1]);
-        }
+        for (int e = 0; e < 4; ++e)
+            d[e & 1] = __ffma2_rn(make_float2(x[8 * ch + 2 * e], x[8 * ch + 2 * e + 1]),
+                                  make_float2(bf16_lo(a[e]), bf16_hi(a[e])), d[e & 1]);
     }
-    return d[0] + d[1];
+    return (d[0].x + d[0].y) + (d[1].x + d[1].y);
 }
 
-// Scale 32 accumulator columns in place.
+// x *= f, and back to tensor memory.
 __device__ __forceinline__ void scale32(uint32_t taddr, float f, float (&x)[32]) {
     uint32_t w[32];
-    ld32f(taddr, x);
+    const float2 ff = make_float2(f, f);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        x[i] *= f;
-        w[i] = __float_as_uint(x[i]);
+    for (int i = 0; i < 32; i += 2) {
+        const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), ff);
+        x[i] = y.x;
+        x[i + 1] = y.y;
+        w[i] = __float_as_uint(y.x);
+        w[i + 1] = __float_as_uint(y.y);
     }
     tmem_st32(taddr, w);
 }
@@ -1275,8 +1304,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb) {
                         float a[16], b[16];
-                        ld16f(ta + hb * 16, a);
-                        ld16f(tb + hb * 16, b);
+                        ld16f2(ta + hb * 16, tb + hb * 16, a, b);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float4 f = reinterpret_cast<const float4*>(F + ib * 32 + hb * 16)[e];
@@ -1293,8 +1321,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb) {
                         float a[16], b[16];
-                        ld16f(ta + hb * 16, a);
-                        ld16f(tb + hb * 16, b);
+                        ld16f2(ta + hb * 16, tb + hb * 16, a, b);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             float pv[2], wv[2];
@@ -1335,10 +1362,11 @@ __global__ void __launch_bounds__(640, 1)
             // the sums of the chunk before are read
             if (g >= 1 && !wait(Cfg::B_SUMFREE, gp ^ 1u, 0x841)) return false;
             if (wide) {
-                float x[32];
+                float x[32], y[32];
+                ld32f2(tmem + Cfg::T2 + dcol, tmem + Cfg::T3 + dcol, x, y);
                 scale32(tmem + Cfg::T2 + dcol, Pre[row], x);
-                scale32(tmem + Cfg::T3 + dcol, Suf[row], x);
-                cj[quarter * C + row] = row_dot32(x, st + Cfg::K + pan * kPanel, row, ch0);
+                scale32(tmem + Cfg::T3 + dcol, Suf[row], y);
+                cj[quarter * C + row] = row_dot32(y, st + Cfg::K + pan * kPanel, row, ch0);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -1347,6 +1375,7 @@ __global__ void __launch_bounds__(640, 1)
             tc_fence_after();
             if (wide) {
                 float x[32];
+                ld32f(tmem + Cfg::T1 + dcol, x);
                 scale32(tmem + Cfg::T1 + dcol, Suf[row], x);
             }
             tmem_wait_st();
@@ -1374,39 +1403,59 @@ __global__ void __launch_bounds__(640, 1)
                     mbar_arrive(empty(s, Cfg::F_E));
                 }
             }
-            // results: into the tile of q, k or dO, whose last reader is done
-            auto result = [&](int tm, int n, int tile, void* dst, bool dot) -> float {
-                float sum = 0.f;
-                if (wide) {
-                    const uint32_t panel = st + tile * Cfg::TILE + pan * kPanel;
-                    float x[32];
-                    ld32f(tmem + tm + dcol, x);
-                    if (dot) sum = row_dot32(x, panel, row, ch0);
-                    if (ch.nv == C) {
-                        put_row32(panel, row, ch0, x);
-                        fence_proxy_async_smem();
-                    } else if (row < ch.nv) {
-                        uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + (ch.row0 + row) * D + quarter * 32);
+            // results: into the tile of q, k or dO, whose last reader is done; returns the dot product with what it held
+            auto result = [&](const float (&x)[32], int tile, void* dst, bool dot) -> float {
+                const uint32_t panel = st + tile * Cfg::TILE + pan * kPanel;
+                const float sum = dot ? row_dot32(x, panel, row, ch0) : 0.f;
+                if (ch.nv == C) {
+                    put_row32(panel, row, ch0, x);
+                    fence_proxy_async_smem();
+                } else if (row < ch.nv) {
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + (ch.row0 + row) * D + quarter * 32);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            out[e] = make_uint4(pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
-                                                pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        out[e] = make_uint4(pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
+                                            pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
                 }
-                tc_fence_before();
-                arrive(Cfg::B_FREE + n);
-                if (wide && lane == 0) mbar_arrive(&bar[Cfg::B_STAGED + n]);
                 return sum;
             };
             if (!wait(Cfg::B_DK, gp, 0x850)) return false;
             tc_fence_after();
-            float u = result(Cfg::T2, 0, Cfg::F_Q, p.dq, true);
-            u -= result(Cfg::T3, 1, Cfg::F_K, p.dk_, true);
+            float u = 0.f;
+            {
+                auto read = [&] {
+                    tc_fence_before();
+                    arrive(Cfg::B_FREE + 0);
+                    if (lane == 0) mbar_arrive(&bar[Cfg::B_FREE + 1]);
+                };
+                if (!wide) {
+                    read();
+                } else {
+                    float x[32], y[32];
+                    ld32f2(tmem + Cfg::T2 + dcol, tmem + Cfg::T3 + dcol, x, y);
+                    read();
+                    u = result(x, Cfg::F_Q, p.dq, true);
+                    arrive(Cfg::B_STAGED + 0);
+                    u -= result(y, Cfg::F_K, p.dk_, true);
+                    arrive(Cfg::B_STAGED + 1);
+                }
+            }
             if (wide) us[quarter * C + row] = u;
             arrive(Cfg::B_SUMS);
             if (!wait(Cfg::B_DV, gp, 0x851)) return false;
             tc_fence_after();
-            result(Cfg::T1, 2, Cfg::F_O, p.dv_, false);
+            {
+                if (!wide) {
+                    arrive(Cfg::B_FREE + 2);
+                } else {
+                    float x[32];
+                    ld32f(tmem + Cfg::T1 + dcol, x);
+                    tc_fence_before();
+                    arrive(Cfg::B_FREE + 2);
+                    result(x, Cfg::F_O, p.dv_, false);
+                    arrive(Cfg::B_STAGED + 2);
+                }
+            }
             return true;
         });
     }
