@@ -125,7 +125,7 @@ cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, 
 
 // CUDA-core kernels: fp32 throughout, fp32 chunk states, any d_k, d_v <= 128.
 constexpr int kGatedSimtChunk = 32;
-cudaError_t launch_gated_states_simt(const GatedProblem& p, bool reverse, cudaStream_t s);
+cudaError_t launch_gated_states_simt(const GatedProblem& p, bool grad, cudaStream_t s);
 cudaError_t launch_gated_out_simt(const GatedProblem& p, cudaStream_t s);
 cudaError_t launch_gated_grad_simt(const GatedProblem& p, cudaStream_t s);
 

@@ -82,7 +82,7 @@ la_status sizes(GatedProblem& p, la_dtype dtype, int B, int H, int64_t T, int dk
 }
 
 la_status place(GatedProblem& p, const Layout& w, void* workspace, size_t bytes) {
-    if (p.groups * w.nc > 0x7fffffffLL) return refuse(LA_ERR_UNSUPPORTED, "too many chunks for one call");
+    if (p.groups * w.nc > 0x7fffffffLL || p.n_units > (1 << 28)) return refuse(LA_ERR_UNSUPPORTED, "too many chunks for one call");
     if (!workspace || bytes < w.bytes || !aligned16(workspace)) {
         char why[128];
         snprintf(why, sizeof(why), "needs a 16-byte aligned workspace of %zu bytes, got %zu", w.bytes,
@@ -218,7 +218,6 @@ la_status la_gated_prefill_backward(const void* q, const void* k, const void* v,
         return e == cudaSuccess ? LA_OK : fail(e);
     }
     e = chunk_offsets(p, w, s);
-    if (e == cudaSuccess) e = launch_gated_states_simt(p, false, s);
     if (e == cudaSuccess) e = launch_gated_states_simt(p, true, s);
     if (e == cudaSuccess) e = launch_gated_grad_simt(p, s);
     return e == cudaSuccess ? LA_OK : fail(e);

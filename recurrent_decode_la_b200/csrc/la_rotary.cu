@@ -67,6 +67,7 @@ __device__ __forceinline__ int packed_place(const int32_t* cu, int num_seqs, int
 // One thread: V pairs (or V passed elements) of one token, heads h0 .. h0 + heads - 1 of both tensors.
 template <typename T, int V, bool INTERLEAVED, bool STREAM>
 __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryProblem p, int items, int heads) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     if (i >= p.B * p.T * items) return;
     const int item = static_cast<int>(i % items);
@@ -155,8 +156,7 @@ cudaError_t rotary_v(const RotaryProblem& p, int num_sms, cudaStream_t s) {
     const bool stream = kWide && bytes > kStreamBytes;
     const auto kern = p.interleaved ? (stream ? rotary_kernel<T, V, true, kWide> : rotary_kernel<T, V, true, false>)
                                     : (stream ? rotary_kernel<T, V, false, kWide> : rotary_kernel<T, V, false, false>);
-    kern<<<grid, kThreads, 0, s>>>(p, items, heads);
-    return cudaGetLastError();
+    return launch_pdl(kern, grid, dim3(kThreads), 0, s, p, items, heads);
 }
 
 __global__ void rotary_init_kernel(float* freq, int rot, double base, int scaling, double factor, double original,
