@@ -60,6 +60,9 @@ struct GatedProblem {
     const int32_t* choff;  // packed: chunks before sequence n, num_seqs + 1 entries
     const int32_t* order;  // packed: the sequences, longest first (nullptr: in their order)
     int64_t nc;            // chunk slots per group
+    // Tensor-core prefill: [0] chunks published, [1] chunks taken, [2] chunks per group (packed), then from kQueueHead
+    // on the published slots, plus one.  All zero at the start but [2].
+    unsigned int* queue;
     void* s_states;        // state at each chunk's start
     void* e_states;        // gradient of the state at each chunk's end
     uint64_t timeout_ns;
@@ -93,6 +96,8 @@ struct GatedChunk {
     int nv;   // its tokens; 0: the slot holds no chunk
 };
 
+constexpr int kQueueHead = 4;
+
 // The chunk of a workspace slot.
 __device__ __forceinline__ GatedChunk gated_chunk(const GatedProblem& p, int64_t slot, int C) {
     const int64_t group = slot / p.nc;
@@ -118,10 +123,11 @@ __device__ __forceinline__ GatedChunk gated_chunk(const GatedProblem& p, int64_t
 // choff[n] = chunks of C tokens in the sequences before n (offsets out of
 // range or decreasing: an empty sequence), n = 0 .. num_seqs.  order (may be
 // nullptr): the sequences by decreasing chunks, ties by index, for at most
-// kMaxGatedOrder of them.
+// kMaxGatedOrder of them.  used (may be nullptr): the chunks of the sequences
+// that fit into nc slots.
 constexpr int kMaxGatedOrder = 1024;
 cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, int C, int32_t* choff, int32_t* order,
-                                 cudaStream_t s);
+                                 int64_t nc, unsigned int* used, cudaStream_t s);
 
 // CUDA-core kernels: fp32 throughout, fp32 chunk states, any d_k, d_v <= 128.
 constexpr int kGatedSimtChunk = 32;
@@ -138,9 +144,10 @@ struct GatedMaps {
     CUtensorMap o;                  // stores: 64 columns x 32 rows
     CUtensorMap dq, dk, dv;         // stores: 64 columns x 128 rows
 };
-// States at the chunk starts; with `grad` also the gradients at the chunk ends.
-cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s);
-cudaError_t launch_gated_out_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);
+// States at the chunk starts and gradients at the chunk ends (for the gradient).
+cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);
+// The whole prefill.
+cudaError_t launch_gated_prefill_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);
 cudaError_t launch_gated_grad_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);
 
 struct RotaryProblem {

@@ -29,12 +29,13 @@ Kernel choose(la_dtype dtype, int64_t max_tokens, int dk, int dv, bool grad) {
 }
 
 // Chunk states in the workspace: packed, first the chunk offsets (num_seqs + 1
-// int32) and the sequences by length (num_seqs int32); then one state per chunk slot, and for the gradient one gradient of
+// int32) and the sequences by length (num_seqs int32); for the tensor-core prefill
+// the queue of published chunks; then one state per chunk slot, and for the gradient one gradient of
 // a state per slot.
 struct Layout {
     int chunk = 0;
     int64_t nc = 0;
-    size_t s = 0, e = 0, bytes = 0;
+    size_t queue = 0, s = 0, e = 0, bytes = 0;
 };
 Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs, bool grad) {
     Layout w;
@@ -43,7 +44,8 @@ Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs
     // a packed sequence begins a chunk of its own
     w.nc = num_seqs > 0 ? T / w.chunk + num_seqs : (T + w.chunk - 1) / w.chunk;
     const size_t states = up256(static_cast<size_t>(groups) * w.nc * dk * dv * (kind == kTc ? 2 : 4));
-    w.s = num_seqs > 0 ? up256((2 * static_cast<size_t>(num_seqs) + 1) * 4) : 0;
+    w.queue = num_seqs > 0 ? up256((2 * static_cast<size_t>(num_seqs) + 1) * 4) : 0;
+    w.s = w.queue + (kind == kTc && !grad ? up256((static_cast<size_t>(groups) * w.nc + kQueueHead) * 4) : 0);
     w.e = w.s + states;
     w.bytes = w.e + (grad ? states : 0);
     return w;
@@ -100,7 +102,8 @@ la_status place(GatedProblem& p, const Layout& w, void* workspace, size_t bytes)
 
 cudaError_t chunk_offsets(const GatedProblem& p, const Layout& w, cudaStream_t s) {
     if (!p.cu) return cudaSuccess;
-    return launch_chunk_offsets(p.cu, p.num_seqs, p.rows, w.chunk, const_cast<int32_t*>(p.choff), const_cast<int32_t*>(p.order), s);
+    return launch_chunk_offsets(p.cu, p.num_seqs, p.rows, w.chunk, const_cast<int32_t*>(p.choff), const_cast<int32_t*>(p.order), w.nc,
+                                p.queue ? p.queue + 2 : nullptr, s);
 }
 
 // The tensor maps of the tensor-core kernels (every tensor 16-byte aligned).
@@ -176,10 +179,10 @@ la_status la_gated_prefill(const void* q, const void* k, const void* v, const vo
     if (kind == kTc) {
         GatedMaps m = {};
         if ((st = maps(m, p, false)) != LA_OK) return st;
-        const int sms = current_sm_count();
-        e = chunk_offsets(p, w, s);
-        if (e == cudaSuccess) e = launch_gated_states_tc(p, m, false, sms, s);
-        if (e == cudaSuccess) e = launch_gated_out_tc(p, m, sms, s);
+        p.queue = reinterpret_cast<unsigned int*>(static_cast<char*>(workspace) + w.queue);
+        e = cudaMemsetAsync(p.queue, 0, w.s - w.queue, s);
+        if (e == cudaSuccess) e = chunk_offsets(p, w, s);
+        if (e == cudaSuccess) e = launch_gated_prefill_tc(p, m, current_sm_count(), s);
         return e == cudaSuccess ? LA_OK : fail(e);
     }
     e = chunk_offsets(p, w, s);
@@ -213,7 +216,7 @@ la_status la_gated_prefill_backward(const void* q, const void* k, const void* v,
         if ((st = maps(m, p, true)) != LA_OK) return st;
         const int sms = current_sm_count();
         e = chunk_offsets(p, w, s);
-        if (e == cudaSuccess) e = launch_gated_states_tc(p, m, true, sms, s);
+        if (e == cudaSuccess) e = launch_gated_states_tc(p, m, sms, s);
         if (e == cudaSuccess) e = launch_gated_grad_tc(p, m, sms, s);
         return e == cudaSuccess ? LA_OK : fail(e);
     }

@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_simt_kernel(const GatedPr
 }
 
 __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __restrict__ cu, int num_seqs, int64_t rows,
-                                                             int chunk, int32_t* __restrict__ choff, int32_t* __restrict__ order) {
+                                                             int chunk, int32_t* __restrict__ choff, int32_t* __restrict__ order, int64_t nc,
+                                                             unsigned int* __restrict__ used) {
     __shared__ int64_t warp_sum[32];
     __shared__ int32_t chunks[kMaxGatedOrder];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -448,6 +449,8 @@ __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __re
             all += warp_sum[i];
         }
         if (n < num_seqs) choff[n] = static_cast<int32_t>(min(base + s - x, static_cast<int64_t>(0x7fffffff)));
+        // the last sequence that ends within the slots
+        if (used != nullptr && n < num_seqs && base + s <= nc) atomicMax(used, static_cast<unsigned int>(base + s));
         before += all;
         __syncthreads();
     }
@@ -490,9 +493,9 @@ cudaError_t chunks_t(const GatedProblem& p, bool grad, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, int chunk, int32_t* choff,
-                                 int32_t* order, cudaStream_t s) {
+                                 int32_t* order, int64_t nc, unsigned int* used, cudaStream_t s) {
     if (num_seqs > kMaxGatedOrder) order = nullptr;
-    return launch_pdl(chunk_offsets_kernel, dim3(1), dim3(1024), 0, s, cu, num_seqs, rows, chunk, choff, order);
+    return launch_pdl(chunk_offsets_kernel, dim3(1), dim3(1024), 0, s, cu, num_seqs, rows, chunk, choff, order, nc, used);
 }
 
 cudaError_t launch_gated_states_simt(const GatedProblem& p, bool grad, cudaStream_t s) {

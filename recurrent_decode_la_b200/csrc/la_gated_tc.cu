@@ -26,6 +26,8 @@
 // Waits are bounded: on expiry the kernel records the device error word, every
 // role winds down, copies and products in flight are drained (bounded), tensor
 // memory is freed and the kernel returns.
+#include <algorithm>
+
 #include "la_device.cuh"
 #include "la_gated.h"
 #include "la_internal.h"
@@ -41,6 +43,24 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Poll until f() holds; gives up like mbar_wait.
+template <typename F>
+__device__ __forceinline__ bool wait_until(uint64_t timeout_ns, volatile int* abort, unsigned int where, F&& f) {
+    if (f()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (f()) return true;
+        if ((it & 15u) == 0) {
+            if (*abort) return false;
+            if (globaltimer_ns() - t0 > timeout_ns) {
+                record_timeout(where);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
 }
 
 // Four log gates (times log2 e) of this lane, tokens 4 lane .. 4 lane + 3 of
@@ -204,22 +224,20 @@ struct StCfg {
                          B_UEMPTY = 4 * NS + NU, B_DONE = 4 * NS + 2 * NU, B_LOEMPTY = B_DONE + 1, NBAR = B_DONE + 1 + NL;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
-    static constexpr int TM_COLS = TS ? 512 : 2 * D;
     // columns of part k of buffer l (TS)
     static constexpr int tm_part(int l, int k) { return NU * D + (l * 3 + k) * 64; }
     static_assert(SMEM <= 232448, "shared memory");
 };
 
+// `worker` of `workers` CTAs; smem 1 KB aligned, tmem all 512 columns.  With p.queue (prefill) the slots are published as
+// their states are stored.
 template <int D>
-__global__ void __launch_bounds__(640, 1)
-    gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items, bool grad) {
+__device__ __forceinline__ void gated_states_body(const GatedMaps& m, const GatedProblem& p, int64_t n_items, bool grad,
+                                                  uint8_t* smem, uint32_t tmem, int64_t worker, int64_t workers) {
     using Cfg = StCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC);
+    unsigned int* stored = reinterpret_cast<unsigned int*>(smem + Cfg::OFF_MISC + 4);  // parts of states stored so far
     float* gam = reinterpret_cast<float*>(smem + Cfg::OFF_GAM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.timeout_ns;
@@ -239,22 +257,16 @@ __global__ void __launch_bounds__(640, 1)
         mbar_init(&bar[Cfg::B_DONE], 1);
         for (int l = 0; l < Cfg::NL; ++l) mbar_init(&bar[Cfg::B_LOEMPTY + l], 1);
         *abort_flag = 0;
+        *stored = 0;
         fence_barrier_init();
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, Cfg::TM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
 
     // Calls f(unit, its state, reverse) for every item of this CTA until f gives up.
     auto items = [&](auto&& f) {
         for (int64_t k = 0;; ++k) {
-            const int64_t i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if (k * gridDim.x >= n_items) return true;
+            const int64_t i = k * workers + (k & 1 ? workers - 1 - worker : worker);
+            if (k * workers >= n_items) return true;
             if (i >= n_items) continue;
             int64_t u = grad ? i >> 1 : i;
             if (p.order != nullptr) u = static_cast<int64_t>(p.order[u / p.H]) * p.H + u % p.H;
@@ -385,6 +397,26 @@ __global__ void __launch_bounds__(640, 1)
             if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
             return true;
         });
+    } else if (warp == 3) {
+        // publish a chunk's slot once every part of its state is in global memory
+        if (lane == 0 && p.queue != nullptr) {
+            walk([&](const GatedUnit& un, bool, int c, int, int64_t g) {
+                const unsigned int want = static_cast<unsigned int>(g + 1) * (4 * Cfg::NPAN);
+                if (!wait_until(tmo, abort_flag, 0x650, [&] {
+                        unsigned int have;
+                        asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(have) : "r"(smem_u32(stored)) : "memory");
+                        return static_cast<int>(have - want) >= 0;
+                    }))
+                    return false;
+                __threadfence();
+                const unsigned int at = atomicAdd(&p.queue[0], 1u);
+                asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.queue + kQueueHead + at),
+                             "r"(static_cast<unsigned int>(un.slot0 + c) + 1u)
+                             : "memory");
+                return true;
+            });
+        }
+        __syncwarp();
     } else if (warp >= 4 && warp < 12) {
         walk([&](const GatedUnit&, bool, int, int nv, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
@@ -499,6 +531,9 @@ __global__ void __launch_bounds__(640, 1)
         constexpr int kRows = D / 4;  // rows of this warp
         float S[64];
         int64_t g = 0;
+        auto count_stored = [&] {
+            asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(stored)) : "memory");
+        };
         items([&](const GatedUnit& un, int64_t u, bool rev) {
             const int nch = (un.len + C - 1) / C;
             if (nch == 0) return true;
@@ -534,6 +569,10 @@ __global__ void __launch_bounds__(640, 1)
                     const int off = half * Cfg::SB_PANEL + sub * kRows * 128;
                     bulk_store(slots + static_cast<int64_t>(c) * Cfg::SB + off, smem + Cfg::OFF_SB + off, kRows * 128);
                     bulk_commit_group();
+                    if (g > 0) {  // the part of the chunk before is in global memory
+                        bulk_wait_group<1>();
+                        count_stored();
+                    }
                 }
                 if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) return false;
                 tc_fence_after();
@@ -557,15 +596,18 @@ __global__ void __launch_bounds__(640, 1)
             }
             return true;
         });
-        if (lane == 0) bulk_wait_group<0>();
+        if (lane == 0) {
+            bulk_wait_group<0>();
+            if (g > 0) count_stored();
+        }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, Cfg::TM_COLS);
-    }
+    tc_fence_after();
+    if (threadIdx.x == 0)
+        for (int b = 0; b < Cfg::NBAR; ++b) mbar_inval(&bar[b]);
+    __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
@@ -592,10 +634,13 @@ struct OutCfg {
     static constexpr int OFF_SB = NS * STAGE;
     static constexpr int OFF_G = OFF_SB + SB;  // [NS]: 128 prefix sums, 96 column factors (the last block needs none)
     static constexpr int G_BYTES = (C + 96) * 4;
-    static constexpr int OFF_BAR = OFF_G + NS * G_BYTES;
+    static constexpr int kRing = NS;  // published chunks
+    static constexpr int OFF_RING = OFF_G + NS * G_BYTES;
+    static constexpr int OFF_BAR = OFF_RING + kRing * 16;
     static constexpr int B_FULL = 0, B_EMPTY = NS, B_GFULL = 2 * NS, B_SFULL = 3 * NS, B_SEMPTY = 3 * NS + 1,
                          B_AFULL = 3 * NS + 2, B_PFULL = 3 * NS + 4, B_OFULL = 3 * NS + 6, B_OEMPTY = 3 * NS + 7,
-                         B_DONE = 3 * NS + 8, B_PEMPTY = 3 * NS + 10, NBAR = 3 * NS + 12;
+                         B_DONE = 3 * NS + 8, B_PEMPTY = 3 * NS + 10, B_UFULL = 3 * NS + 12, B_UEMPTY = B_UFULL + NS,
+                         NBAR = B_UEMPTY + NS;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TM_A = 0, TM_O1 = 256, TM_O2 = 256 + D;
@@ -603,15 +648,11 @@ struct OutCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(640, 1)
-    gated_out_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_slots) {
+__device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedProblem& p, uint8_t* smem, uint32_t tmem) {
     using Cfg = OutCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC);
+    volatile int4* ring = reinterpret_cast<volatile int4*>(smem + Cfg::OFF_RING);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.timeout_ns;
     const uint32_t sbase = smem_u32(smem);
@@ -633,73 +674,95 @@ __global__ void __launch_bounds__(640, 1)
         mbar_init(&bar[Cfg::B_OEMPTY], 4 * Cfg::NPAN);
         mbar_init(&bar[Cfg::B_DONE], 1);
         mbar_init(&bar[Cfg::B_DONE + 1], 1);
+        for (int r = 0; r < Cfg::kRing; ++r) {
+            mbar_init(&bar[Cfg::B_UFULL + r], 1);
+            mbar_init(&bar[Cfg::B_UEMPTY + r], 3 + 8 + 4 * Cfg::NPAN);
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
 
-    auto walk = [&](auto&& f) -> bool {
-        int64_t g = 0;
-        for (int64_t i = blockIdx.x; i < n_slots; i += gridDim.x) {
-            const GatedChunk ch = gated_chunk(p, i, C);
-            if (ch.nv <= 0) continue;
-            if (!f(ch, i, g)) return false;
-            ++g;
+    // Calls f(chunk, chunks before it) for every chunk that the producer publishes in the ring (`one`: by lane 0 alone).
+    auto walk = [&](bool one, auto&& f) -> bool {
+        for (int64_t g = 0;; ++g) {
+            const int r = static_cast<int>(g % Cfg::kRing);
+            const uint32_t ph = static_cast<uint32_t>(g / Cfg::kRing) & 1;
+            if (!(one ? mbar_wait(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x770)
+                      : mbar_wait_warp(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x771)))
+                return false;
+            const int row = ring[r].x, group = ring[r].y, nv = ring[r].z;
+            if (!one) __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[Cfg::B_UEMPTY + r]);
+            if (nv <= 0) return true;
+            if (!f(GatedChunk{group * p.rows + row, group, row, nv}, g)) return false;
         }
-        return true;
     };
 
     if (warp == 0) {
         if (lane == 0) {
-            int64_t started = 0;
-            const bool ok = walk([&](const GatedChunk& ch, int64_t slot, int64_t g) {
-                const int s = static_cast<int>(g % Cfg::NS);
-                if (g >= Cfg::NS &&
-                    !mbar_wait(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x700 + s))
-                    return false;
-                mbar_arrive_expect_tx(&bar[Cfg::B_FULL + s], 3 * Cfg::TILE);
-                uint8_t* st = smem + s * Cfg::STAGE;
-#pragma unroll
-                for (int pn = 0; pn < Cfg::NPAN; ++pn) {
-                    tma_load_3d(st + pn * kPanel, &m.q, &bar[Cfg::B_FULL + s], pn * 64, ch.row, ch.group);
-                    tma_load_3d(st + Cfg::TILE + pn * kPanel, &m.k, &bar[Cfg::B_FULL + s], pn * 64, ch.row, ch.group);
-                    tma_load_3d(st + 2 * Cfg::TILE + pn * kPanel, &m.v, &bar[Cfg::B_FULL + s], pn * 64, ch.row,
-                                ch.group);
-                }
-                started = g + 1;
-                if (g >= 1 && !mbar_wait(&bar[Cfg::B_SEMPTY], (g + 1) & 1, abort_flag, tmo, 0x708)) return false;
-                mbar_arrive_expect_tx(&bar[Cfg::B_SFULL], Cfg::SB);
-                bulk_load(smem + Cfg::OFF_SB, static_cast<const uint8_t*>(p.s_states) + slot * Cfg::SB, Cfg::SB,
-                          &bar[Cfg::B_SFULL]);
-                // the next chunk into L2, while its stage is still in use
-                const int64_t next = slot + gridDim.x;
-                if (next < n_slots) {
-                    const GatedChunk c2 = gated_chunk(p, next, C);
-                    if (c2.nv > 0) {
+            int64_t started = 0, loaded = 0;  // chunks whose tiles, whose state are under way
+            const int64_t total = p.cu ? static_cast<int64_t>(p.queue[2]) * p.H : p.groups * p.nc;
+            const bool ok = [&] {
+                for (int64_t g = 0;; ++g) {
+                    // the next chunk in the order in which the states come to be
+                    const unsigned int at = atomicAdd(&p.queue[1], 1u);
+                    unsigned int entry = 0;
+                    GatedChunk ch = {0, 0, 0, 0};
+                    if (at < total) {
+                        if (!wait_until(tmo, abort_flag, 0x772, [&] {
+                                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];"
+                                             : "=r"(entry)
+                                             : "l"(p.queue + kQueueHead + at)
+                                             : "memory");
+                                if (entry == 0) __nanosleep(40);
+                                return entry != 0;
+                            }))
+                            return false;
+                        asm volatile("fence.proxy.async;" ::: "memory");  // the state: another SM's writes, read by a copy
+                        ch = gated_chunk(p, entry - 1, C);
+                    }
+                    const int r = static_cast<int>(g % Cfg::kRing), s = static_cast<int>(g % Cfg::NS);
+                    if (g >= Cfg::kRing &&
+                        !mbar_wait(&bar[Cfg::B_UEMPTY + r], ((g / Cfg::kRing) + 1) & 1, abort_flag, tmo, 0x773))
+                        return false;
+                    ring[r].x = ch.row;
+                    ring[r].y = ch.group;
+                    ring[r].z = ch.nv;
+                    mbar_arrive(&bar[Cfg::B_UFULL + r]);
+                    if (ch.nv <= 0) return true;
+                    const uint8_t* state = static_cast<const uint8_t*>(p.s_states) + static_cast<int64_t>(entry - 1) * Cfg::SB;
+                    if (g >= Cfg::NS) {
+                        // into L2 while the stage is still in use
 #pragma unroll
                         for (int pn = 0; pn < Cfg::NPAN; ++pn) {
-                            tma_prefetch_l2_3d(&m.q, pn * 64, c2.row, c2.group);
-                            tma_prefetch_l2_3d(&m.k, pn * 64, c2.row, c2.group);
-                            tma_prefetch_l2_3d(&m.v, pn * 64, c2.row, c2.group);
+                            tma_prefetch_l2_3d(&m.q, pn * 64, ch.row, ch.group);
+                            tma_prefetch_l2_3d(&m.k, pn * 64, ch.row, ch.group);
+                            tma_prefetch_l2_3d(&m.v, pn * 64, ch.row, ch.group);
                         }
-                        bulk_prefetch_l2(static_cast<const uint8_t*>(p.s_states) + next * Cfg::SB, Cfg::SB);
+                        if (!mbar_wait(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x700 + s))
+                            return false;
                     }
+                    mbar_arrive_expect_tx(&bar[Cfg::B_FULL + s], 3 * Cfg::TILE);
+                    uint8_t* st = smem + s * Cfg::STAGE;
+#pragma unroll
+                    for (int pn = 0; pn < Cfg::NPAN; ++pn) {
+                        tma_load_3d(st + pn * kPanel, &m.q, &bar[Cfg::B_FULL + s], pn * 64, ch.row, ch.group);
+                        tma_load_3d(st + Cfg::TILE + pn * kPanel, &m.k, &bar[Cfg::B_FULL + s], pn * 64, ch.row, ch.group);
+                        tma_load_3d(st + 2 * Cfg::TILE + pn * kPanel, &m.v, &bar[Cfg::B_FULL + s], pn * 64, ch.row,
+                                    ch.group);
+                    }
+                    started = g + 1;
+                    if (g >= 1 && !mbar_wait(&bar[Cfg::B_SEMPTY], (g + 1) & 1, abort_flag, tmo, 0x708)) return false;
+                    mbar_arrive_expect_tx(&bar[Cfg::B_SFULL], Cfg::SB);
+                    bulk_load(smem + Cfg::OFF_SB, state, Cfg::SB, &bar[Cfg::B_SFULL]);
+                    loaded = g + 1;
                 }
-                return true;
-            });
+            }();
             if (!ok || *abort_flag) {
                 for (int64_t g = started > Cfg::NS ? started - Cfg::NS : 0; g < started; ++g)
                     mbar_wait_drain(&bar[Cfg::B_FULL + g % Cfg::NS], (g / Cfg::NS) & 1, tmo);
-                // the last state copy was started for chunk started - 1, or, if its slot was not free, started - 2
-                if (started >= 2) mbar_wait_drain(&bar[Cfg::B_SFULL], (started - 2) & 1, tmo);
-                if (ok && started >= 1) mbar_wait_drain(&bar[Cfg::B_SFULL], (started - 1) & 1, tmo);
+                if (loaded >= 1) mbar_wait_drain(&bar[Cfg::B_SFULL], (loaded - 1) & 1, tmo);
             }
         }
     } else if (warp == 1 || warp == 3) {
@@ -746,9 +809,9 @@ __global__ void __launch_bounds__(640, 1)
                 return true;
             };
             if (warp == 3)
-                walk([&](const GatedChunk&, int64_t, int64_t g) { return scores(g); });
+                walk(true, [&](const GatedChunk&, int64_t g) { return scores(g); });
             else
-                walk([&](const GatedChunk&, int64_t, int64_t g) { return output(g); });
+                walk(true, [&](const GatedChunk&, int64_t g) { return output(g); });
             if (issued) {
                 mma_commit(&bar[Cfg::B_DONE + (warp == 3)]);
                 mbar_wait_drain(&bar[Cfg::B_DONE + (warp == 3)], 0, tmo);
@@ -756,7 +819,7 @@ __global__ void __launch_bounds__(640, 1)
         }
         __syncwarp();
     } else if (warp == 2) {
-        walk([&](const GatedChunk& ch, int64_t, int64_t g) {
+        walk(false, [&](const GatedChunk& ch, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
             float x[4], G[4];
             load_gates(p, ch.row0, ch.nv, x);
@@ -777,7 +840,7 @@ __global__ void __launch_bounds__(640, 1)
         });
     } else if (warp >= 4 && warp < 12) {
         const int sub = warp & 3, half = (warp - 4) >> 2, row = sub * 32 + lane;
-        walk([&](const GatedChunk&, int64_t, int64_t g) {
+        walk(false, [&](const GatedChunk&, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
             if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x750 + s)) return false;
             if (!mbar_wait_warp(&bar[Cfg::B_AFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x758 + b)) return false;
@@ -829,7 +892,7 @@ __global__ void __launch_bounds__(640, 1)
     } else if (warp >= 12 && warp < 12 + 4 * Cfg::NPAN) {
         const int sub = warp & 3, half = (warp - 12) >> 2, row = sub * 32 + lane;
         const uint32_t lane_off = (static_cast<uint32_t>(sub * 32) << 16) + half * 64;
-        walk([&](const GatedChunk& ch, int64_t, int64_t g) {
+        walk(false, [&](const GatedChunk& ch, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
             if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x760 + s)) return false;
             const float f = ex2(reinterpret_cast<const float*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES)[row]);
@@ -874,10 +937,54 @@ __global__ void __launch_bounds__(640, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
+    tc_fence_after();
+}
+
+// Shared memory of a kernel, 1 KB aligned, and all of its tensor memory.
+__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* raw) {
+    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+}
+__device__ __forceinline__ uint32_t take_tmem(uint8_t* smem) {
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem);
+    if (threadIdx.x < 32) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    __syncthreads();
+    return tmem;
+}
+__device__ __forceinline__ void give_tmem(uint32_t tmem) {
+    if (threadIdx.x < 32) tmem_dealloc(tmem, 512);
+}
+
+// The states of the gradient, both directions.
+template <int D>
+__global__ void __launch_bounds__(640, 1)
+    gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = aligned_smem(smem_raw);
+    const uint32_t tmem = take_tmem(smem);
+    gated_states_body<D>(m, p, n_items, true, smem, tmem, blockIdx.x, gridDim.x);
+    give_tmem(tmem);
+}
+
+// The prefill in one launch: the first n_state CTAs make the states and publish each chunk as its state is stored; the
+// others, and those when they are done, take the chunks in that order.  So K, V and the states come from L2 the second
+// time, and the serial phase of few long sequences overlaps the other.  Only the later CTAs wait, for ones that the
+// device starts before them.
+template <int D>
+__global__ void __launch_bounds__(640, 1)
+    gated_prefill_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items, int n_state) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = aligned_smem(smem_raw);
+    const uint32_t tmem = take_tmem(smem);
+    if (static_cast<int>(blockIdx.x) < n_state) gated_states_body<D>(m, p, n_items, false, smem, tmem, blockIdx.x, n_state);
+    gated_out_body<D>(m, p, smem, tmem);
+    give_tmem(tmem);
 }
 
 // ---------------------------------------------------------------------------
@@ -1475,21 +1582,28 @@ cudaError_t raise_smem(PerDeviceOnce& once, F kern, int bytes) {
 unsigned grid_for(int64_t items, int num_sms) { return static_cast<unsigned>(items < num_sms ? items : num_sms); }
 
 template <int D>
-cudaError_t states_d(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s) {
+cudaError_t states_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
     cudaError_t e = raise_smem(once, gated_states_tc_kernel<D>, StCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t items = grad ? 2 * p.n_units : p.n_units;
-    gated_states_tc_kernel<D><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items, grad);
+    const int64_t items = 2 * p.n_units;
+    gated_states_tc_kernel<D><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items);
     return cudaGetLastError();
 }
 template <int D>
-cudaError_t out_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+cudaError_t prefill_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+    constexpr int kSmem = StCfg<D>::SMEM > OutCfg<D>::SMEM ? StCfg<D>::SMEM : OutCfg<D>::SMEM;
     static PerDeviceOnce once;
-    cudaError_t e = raise_smem(once, gated_out_tc_kernel<D>, OutCfg<D>::SMEM);
+    cudaError_t e = raise_smem(once, gated_prefill_tc_kernel<D>, kSmem);
     if (e != cudaSuccess) return e;
+    // A chunk's state takes about three quarters of the time of its output: as many CTAs as make the states in the
+    // fewest rounds on 45 % of the device.
+    const int most = std::max(1, num_sms * 45 / 100);
+    const int64_t rounds = (p.n_units + most - 1) / most;
+    const int n_state = static_cast<int>((p.n_units + rounds - 1) / rounds);
     const int64_t slots = p.groups * p.nc;
-    gated_out_tc_kernel<D><<<grid_for(slots, num_sms), OutCfg<D>::kThreads, OutCfg<D>::SMEM, s>>>(m, p, slots);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(num_sms, n_state + slots)));
+    gated_prefill_tc_kernel<D><<<grid, OutCfg<D>::kThreads, kSmem, s>>>(m, p, p.n_units, n_state);
     return cudaGetLastError();
 }
 template <int D>
@@ -1504,11 +1618,11 @@ cudaError_t grad_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaS
 
 }  // namespace
 
-cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s) {
-    return p.dk == 128 ? states_d<128>(p, m, grad, num_sms, s) : states_d<64>(p, m, grad, num_sms, s);
+cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+    return p.dk == 128 ? states_d<128>(p, m, num_sms, s) : states_d<64>(p, m, num_sms, s);
 }
-cudaError_t launch_gated_out_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
-    return p.dk == 128 ? out_d<128>(p, m, num_sms, s) : out_d<64>(p, m, num_sms, s);
+cudaError_t launch_gated_prefill_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+    return p.dk == 128 ? prefill_d<128>(p, m, num_sms, s) : prefill_d<64>(p, m, num_sms, s);
 }
 cudaError_t launch_gated_grad_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
     return p.dk == 128 ? grad_d<128>(p, m, num_sms, s) : grad_d<64>(p, m, num_sms, s);

@@ -68,8 +68,9 @@ def test_workspace_sizes(lib):
     assert la.la_gated_prefill_backward_workspace_size(torch.float32, 2, 3, 65, 64, 32) == 2 * 2 * 3 * 3 * 64 * 32 * 4
     # packed: two chunks of 64 rows and one more for each of five sequences, after six offsets
     assert la.la_gated_prefill_workspace_size(torch.float32, 1, 3, 64, 64, 32, 5) == 256 + 3 * 7 * 64 * 32 * 4
-    # tensor cores: a bf16 state per chunk of 128
-    assert la.la_gated_prefill_workspace_size(torch.bfloat16, 2, 3, 129, 64, 64) == 2 * 2 * 3 * 64 * 64 * 2
+    # tensor cores: a bf16 state per chunk of 128, after the queue of chunks; without the queue twice for the gradient
+    assert la.la_gated_prefill_workspace_size(torch.bfloat16, 2, 3, 129, 64, 64) == 256 + 2 * 2 * 3 * 64 * 64 * 2
+    assert la.la_gated_prefill_backward_workspace_size(torch.bfloat16, 2, 3, 129, 64, 64) == 2 * 2 * 2 * 3 * 64 * 64 * 2
     # the few-token kernel needs none, unless the longest packed sequence is not known
     assert la.la_gated_prefill_workspace_size(torch.bfloat16, 4, 4, 16, 128, 128) == 0
     assert la.la_gated_prefill_workspace_size(torch.bfloat16, 1, 4, 16, 128, 128, 2) > 0
