@@ -45,6 +45,34 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+#ifndef NSLEEP
+#define NSLEEP 32
+#endif
+// mbar_wait with a pause between polls.  Twenty warps share an SM's issue slots here, and a warp that polls without pause
+// takes them from those that compute: the scores of a block took ten clocks an instruction.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns,
+                                         unsigned int where) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (NSLEEP) __nanosleep(NSLEEP);
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort) return false;
+            if (globaltimer_ns() - t0 > timeout_ns) {
+                record_timeout(where);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns,
+                                          unsigned int where) {
+    const bool ok = wait_one(bar, parity, abort, timeout_ns, where);
+    return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;
+}
+
 // Poll until f() holds; gives up like mbar_wait.
 template <typename F>
 __device__ __forceinline__ bool wait_until(uint64_t timeout_ns, volatile int* abort, unsigned int where, F&& f) {
@@ -124,24 +152,24 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int nv) {
     }
 }
 
-// 64 fp32 values of a row -> bf16 into a 128-byte swizzled panel row.
-__device__ __forceinline__ void put_row32(uint32_t panel, int row, int chunk0, const float (&x)[32]) {
+// The kernels below work on accumulator rows 16 columns at a time, in loops that are kept rolled: twenty warps in different
+// roles share the instruction cache, and with whole rows unrolled a warp waited for instructions ten clocks each.
+
+// 16 fp32 values of a row -> bf16, two 16-byte pieces of a 128-byte swizzled panel row.
+__device__ __forceinline__ void put_row16(uint32_t panel, int row, int chunk0, const float (&x)[16]) {
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch)
+    for (int ch = 0; ch < 2; ++ch)
         st_shared_v4(panel + sw128_off(row, chunk0 + ch), pack_bf16x2(x[8 * ch], x[8 * ch + 1]),
                      pack_bf16x2(x[8 * ch + 2], x[8 * ch + 3]), pack_bf16x2(x[8 * ch + 4], x[8 * ch + 5]),
                      pack_bf16x2(x[8 * ch + 6], x[8 * ch + 7]));
 }
-
-__device__ __forceinline__ void ld32f(uint32_t taddr, float (&x)[32]) {
-    uint32_t r[32];
-    tmem_ld32(taddr, r);
-    tmem_wait_ld();
+// The same straight to global memory.
+__device__ __forceinline__ void put_row16(uint16_t* out, const float (&x)[16]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        asm volatile("" : "+r"(r[i]));  // not used before the wait
-        x[i] = __uint_as_float(r[i]);
-    }
+    for (int ch = 0; ch < 2; ++ch)
+        reinterpret_cast<uint4*>(out)[ch] =
+            make_uint4(pack_bf16x2(x[8 * ch], x[8 * ch + 1]), pack_bf16x2(x[8 * ch + 2], x[8 * ch + 3]),
+                       pack_bf16x2(x[8 * ch + 4], x[8 * ch + 5]), pack_bf16x2(x[8 * ch + 6], x[8 * ch + 7]));
 }
 
 __device__ __forceinline__ void ld16f(uint32_t taddr, float (&x)[16]) {
@@ -163,19 +191,6 @@ __device__ __forceinline__ void ld16f2(uint32_t ta, uint32_t tb, float (&x)[16],
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        asm volatile("" : "+r"(r[i]), "+r"(q[i]));
-        x[i] = __uint_as_float(r[i]);
-        y[i] = __uint_as_float(q[i]);
-    }
-}
-
-__device__ __forceinline__ void ld32f2(uint32_t ta, uint32_t tb, float (&x)[32], float (&y)[32]) {
-    uint32_t r[32], q[32];
-    tmem_ld32(ta, r);
-    tmem_ld32(tb, q);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
         asm volatile("" : "+r"(r[i]), "+r"(q[i]));
         x[i] = __uint_as_float(r[i]);
         y[i] = __uint_as_float(q[i]);
@@ -297,7 +312,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
             const bool ok = walk([&](const GatedUnit& un, bool rev, int c, int, int64_t g) {
                 const int s = static_cast<int>(g % Cfg::NS);
                 if (g >= Cfg::NS &&
-                    !mbar_wait(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x600 + s))
+                    !wait_one(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x600 + s))
                     return false;
                 const CUtensorMap* mx = rev ? &m.q : &m.k;
                 const CUtensorMap* my = rev ? &m.d_o : &m.v;
@@ -332,9 +347,9 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
             bool issued = false;
             walk([&](const GatedUnit&, bool, int, int, int64_t g) {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g % Cfg::NU), l = static_cast<int>(g % Cfg::NL);
-                if (!mbar_wait(&bar[Cfg::B_SCALED + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x610 + s)) return false;
+                if (!wait_one(&bar[Cfg::B_SCALED + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x610 + s)) return false;
                 if (g >= Cfg::NU &&
-                    !mbar_wait(&bar[Cfg::B_UEMPTY + b], ((g / Cfg::NU) + 1) & 1, abort_flag, tmo, 0x618 + b))
+                    !wait_one(&bar[Cfg::B_UEMPTY + b], ((g / Cfg::NU) + 1) & 1, abort_flag, tmo, 0x618 + b))
                     return false;
                 tc_fence_after();
                 const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE,
@@ -377,7 +392,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
             } else {
                 scan_down(x, w, all);
             }
-            if (g >= 2 && !mbar_wait_warp(&bar[Cfg::B_SCALED + (g - 2) % Cfg::NS], ((g - 2) / Cfg::NS) & 1, abort_flag,
+            if (g >= 2 && !wait_warp(&bar[Cfg::B_SCALED + (g - 2) % Cfg::NS], ((g - 2) / Cfg::NS) & 1, abort_flag,
                                           tmo, 0x620 + s))
                 return false;
             uint2* o = reinterpret_cast<uint2*>(smem + Cfg::OFF_W + (g % Cfg::NW) * 3 * C * 2);
@@ -421,8 +436,8 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         walk([&](const GatedUnit&, bool, int, int nv, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
             const uint32_t ph = (g / Cfg::NS) & 1;
-            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], ph, abort_flag, tmo, 0x630 + s)) return false;
-            if (!mbar_wait_warp(&bar[Cfg::B_FULL + s], ph, abort_flag, tmo, 0x638 + s)) return false;
+            if (!wait_warp(&bar[Cfg::B_GFULL + s], ph, abort_flag, tmo, 0x630 + s)) return false;
+            if (!wait_warp(&bar[Cfg::B_FULL + s], ph, abort_flag, tmo, 0x638 + s)) return false;
             const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE;
             const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + Cfg::OFF_W + (g % Cfg::NW) * 3 * C * 2);
             // w x = hi + mid + lo for two values at a time, in paired bf16 arithmetic.  A product of two 8-bit
@@ -446,11 +461,11 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 if (nv < C)
                     for (int row = nv + (warp - 4); row < C; row += 8)
                         if (lane < 16) st_shared_v4(y + (lane >> 3) * kPanel + row * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
-                if (!lofree && !mbar_wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
+                if (!lofree && !wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
                     return false;
                 tc_fence_after();
                 const uint32_t tp = tmem + Cfg::tm_part(g % Cfg::NL, 0) + half * 32 + (static_cast<uint32_t>(sub * 32) << 16);
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < 4; kk += 2) {  // 32 tokens
                     uint32_t part[2][3][8];
 #pragma unroll
@@ -491,7 +506,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 tc_fence_before();
             } else {
                 const uint32_t lo = sbase + Cfg::OFF_LO + (g % Cfg::NL) * 2 * Cfg::TILE;
-                if (!lofree && !mbar_wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
+                if (!lofree && !wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
                     return false;
                 // warp w takes rows 16 (w - 4) ..; its lanes four rows of eight 16-byte pieces at a time
                 const int r0 = (warp - 4) * 16 + (lane >> 3);
@@ -574,7 +589,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                         count_stored();
                     }
                 }
-                if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) return false;
+                if (!wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) return false;
                 tc_fence_after();
                 const float gamma = gam[g % Cfg::kGam];
 #pragma unroll
@@ -688,8 +703,8 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
         for (int64_t g = 0;; ++g) {
             const int r = static_cast<int>(g % Cfg::kRing);
             const uint32_t ph = static_cast<uint32_t>(g / Cfg::kRing) & 1;
-            if (!(one ? mbar_wait(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x770)
-                      : mbar_wait_warp(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x771)))
+            if (!(one ? wait_one(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x770)
+                      : wait_warp(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x771)))
                 return false;
             const int row = ring[r].x, group = ring[r].y, nv = ring[r].z;
             if (!one) __syncwarp();
@@ -724,7 +739,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                     }
                     const int r = static_cast<int>(g % Cfg::kRing), s = static_cast<int>(g % Cfg::NS);
                     if (g >= Cfg::kRing &&
-                        !mbar_wait(&bar[Cfg::B_UEMPTY + r], ((g / Cfg::kRing) + 1) & 1, abort_flag, tmo, 0x773))
+                        !wait_one(&bar[Cfg::B_UEMPTY + r], ((g / Cfg::kRing) + 1) & 1, abort_flag, tmo, 0x773))
                         return false;
                     ring[r].x = ch.row;
                     ring[r].y = ch.group;
@@ -740,7 +755,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                             tma_prefetch_l2_3d(&m.k, pn * 64, ch.row, ch.group);
                             tma_prefetch_l2_3d(&m.v, pn * 64, ch.row, ch.group);
                         }
-                        if (!mbar_wait(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x700 + s))
+                        if (!wait_one(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x700 + s))
                             return false;
                     }
                     mbar_arrive_expect_tx(&bar[Cfg::B_FULL + s], 3 * Cfg::TILE);
@@ -753,7 +768,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                                     ch.group);
                     }
                     started = g + 1;
-                    if (g >= 1 && !mbar_wait(&bar[Cfg::B_SEMPTY], (g + 1) & 1, abort_flag, tmo, 0x708)) return false;
+                    if (g >= 1 && !wait_one(&bar[Cfg::B_SEMPTY], (g + 1) & 1, abort_flag, tmo, 0x708)) return false;
                     mbar_arrive_expect_tx(&bar[Cfg::B_SFULL], Cfg::SB);
                     bulk_load(smem + Cfg::OFF_SB, state, Cfg::SB, &bar[Cfg::B_SFULL]);
                     loaded = g + 1;
@@ -772,9 +787,9 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
             bool issued = false;
             auto scores = [&](int64_t g) -> bool {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
-                if (!mbar_wait(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x710 + s)) return false;
+                if (!wait_one(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x710 + s)) return false;
                 // the buffer's last P, of chunk g - 2, is used up
-                if (g >= 2 && !mbar_wait(&bar[Cfg::B_PEMPTY + b], ((g >> 1) + 1) & 1, abort_flag, tmo, 0x718)) return false;
+                if (g >= 2 && !wait_one(&bar[Cfg::B_PEMPTY + b], ((g >> 1) + 1) & 1, abort_flag, tmo, 0x718)) return false;
                 tc_fence_after();
                 const uint32_t q = sbase + s * Cfg::STAGE, k = q + Cfg::TILE;
 #pragma unroll
@@ -787,9 +802,9 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
             };
             auto output = [&](int64_t g) -> bool {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
-                if (g >= 1 && !mbar_wait(&bar[Cfg::B_OEMPTY], (g + 1) & 1, abort_flag, tmo, 0x720)) return false;
-                if (!mbar_wait(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x724)) return false;
-                if (!mbar_wait(&bar[Cfg::B_SFULL], g & 1, abort_flag, tmo, 0x728)) return false;
+                if (g >= 1 && !wait_one(&bar[Cfg::B_OEMPTY], (g + 1) & 1, abort_flag, tmo, 0x720)) return false;
+                if (!wait_one(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x724)) return false;
+                if (!wait_one(&bar[Cfg::B_SFULL], g & 1, abort_flag, tmo, 0x728)) return false;
                 tc_fence_after();
                 const uint32_t q = sbase + s * Cfg::STAGE, v = q + 2 * Cfg::TILE, sb = sbase + Cfg::OFF_SB;
 #pragma unroll
@@ -798,7 +813,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                                 sdesc_sw128(sb + ks * 2048, Cfg::SB_PANEL, 1024), kIdO, ks > 0);
                 mma_commit(&bar[Cfg::B_SEMPTY]);
                 issued = true;
-                if (!mbar_wait(&bar[Cfg::B_PFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x730 + b)) return false;
+                if (!wait_one(&bar[Cfg::B_PFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x730 + b)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks)
@@ -826,7 +841,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
             scan_up(x, G);
             const float R = __shfl_sync(0xffffffffu, G[3], lane | 7);  // prefix at the end of the 32-token block
             // tiles landed: the slot's last readers are done
-            if (!mbar_wait_warp(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x740 + s)) return false;
+            if (!wait_warp(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x740 + s)) return false;
             float4* o = reinterpret_cast<float4*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES);
             o[lane] = make_float4(G[0], G[1], G[2], G[3]);
             if (lane < 24) o[32 + lane] = make_float4(ex2(R - G[0]), ex2(R - G[1]), ex2(R - G[2]), ex2(R - G[3]));
@@ -842,47 +857,48 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
         const int sub = warp & 3, half = (warp - 4) >> 2, row = sub * 32 + lane;
         walk(false, [&](const GatedChunk&, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
-            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x750 + s)) return false;
-            if (!mbar_wait_warp(&bar[Cfg::B_AFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x758 + b)) return false;
+            if (!wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x750 + s)) return false;
+            if (!wait_warp(&bar[Cfg::B_AFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x758 + b)) return false;
             tc_fence_after();
             const float* G = reinterpret_cast<const float*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES);
             const float* F = G + C;
             // scores of this half's keys in columns 64 half ..; P goes to the first 32 of them
             const uint32_t tm = tmem + Cfg::TM_A + b * C + half * 64 + (static_cast<uint32_t>(sub * 32) << 16);
             const float Gi = G[row];
-            uint32_t w[32];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int jb = 2 * half + q;  // block of 32 keys; warp-uniform cases
+#pragma unroll 1
+            for (int pc = 0; pc < 4; ++pc) {  // 16 keys; warp-uniform cases
+                const int jb = 2 * half + (pc >> 1), j0 = jb * 32 + (pc & 1) * 16;
+                uint32_t w[8];
                 if (jb > sub) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[16 * q + e] = 0u;
-                    continue;
-                }
-                float a[32];
-                ld32f(tm + q * 32, a);
-                if (jb < sub) {
-                    const float f = ex2(Gi - G[jb * 32 + 31]);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float4 c = reinterpret_cast<const float4*>(F + jb * 32)[e];
-                        w[16 * q + 2 * e] = pack_bf16x2(a[4 * e] * (f * c.x), a[4 * e + 1] * (f * c.y));
-                        w[16 * q + 2 * e + 1] = pack_bf16x2(a[4 * e + 2] * (f * c.z), a[4 * e + 3] * (f * c.w));
-                    }
+                    for (int e = 0; e < 8; ++e) w[e] = 0u;
                 } else {
+                    float a[16];
+                    ld16f(tm + pc * 16, a);
+                    if (jb < sub) {
+                        const float f = ex2(Gi - G[jb * 32 + 31]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float4 c = reinterpret_cast<const float4*>(G + jb * 32)[e];
-                        const float d[4] = {c.x, c.y, c.z, c.w};
-                        float y[4];
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 c = reinterpret_cast<const float4*>(F + j0)[e];
+                            w[2 * e] = pack_bf16x2(a[4 * e] * (f * c.x), a[4 * e + 1] * (f * c.y));
+                            w[2 * e + 1] = pack_bf16x2(a[4 * e + 2] * (f * c.z), a[4 * e + 3] * (f * c.w));
+                        }
+                    } else {
+                        const int last = lane - (pc & 1) * 16;  // keys up to the row's own
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) y[k] = 4 * e + k <= lane ? a[4 * e + k] * ex2(Gi - d[k]) : 0.f;
-                        w[16 * q + 2 * e] = pack_bf16x2(y[0], y[1]);
-                        w[16 * q + 2 * e + 1] = pack_bf16x2(y[2], y[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 c = reinterpret_cast<const float4*>(G + j0)[e];
+                            const float d[4] = {c.x, c.y, c.z, c.w};
+                            float y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] = 4 * e + k <= last ? a[4 * e + k] * ex2(Gi - d[k]) : 0.f;
+                            w[2 * e] = pack_bf16x2(y[0], y[1]);
+                            w[2 * e + 1] = pack_bf16x2(y[2], y[3]);
+                        }
                     }
                 }
+                tmem_st8(tm + pc * 8, w);  // over scores that are read
             }
-            tmem_st32(tm, w);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -894,28 +910,22 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
         const uint32_t lane_off = (static_cast<uint32_t>(sub * 32) << 16) + half * 64;
         walk(false, [&](const GatedChunk& ch, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
-            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x760 + s)) return false;
+            if (!wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x760 + s)) return false;
             const float f = ex2(reinterpret_cast<const float*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES)[row]);
-            if (!mbar_wait_warp(&bar[Cfg::B_OFULL], g & 1, abort_flag, tmo, 0x768)) return false;
+            if (!wait_warp(&bar[Cfg::B_OFULL], g & 1, abort_flag, tmo, 0x768)) return false;
             tc_fence_after();
             const uint32_t panel = sbase + s * Cfg::STAGE + half * kPanel;  // Q, read by both of its products
             uint16_t* out = static_cast<uint16_t*>(p.o) + (ch.row0 + row) * D + half * 64;
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+                float x[16], y[16];
+                ld16f2(tmem + Cfg::TM_O1 + lane_off + h * 16, tmem + Cfg::TM_O2 + lane_off + h * 16, x, y);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32], y[32];
-                ld32f(tmem + Cfg::TM_O1 + lane_off + h * 32, x);
-                ld32f(tmem + Cfg::TM_O2 + lane_off + h * 32, y);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = fmaf(f, x[e], y[e]);
-                if (ch.nv == C) {
-                    put_row32(panel, row, 4 * h, x);
-                } else if (row < ch.nv) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        reinterpret_cast<uint4*>(out + h * 32)[e] =
-                            make_uint4(pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
-                                       pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
-                }
+                for (int e = 0; e < 16; ++e) x[e] = fmaf(f, x[e], y[e]);
+                if (ch.nv == C)
+                    put_row16(panel, row, 2 * h, x);
+                else if (row < ch.nv)
+                    put_row16(out + h * 16, x);
             }
             tc_fence_before();
             fence_proxy_async_smem();
@@ -1042,11 +1052,11 @@ struct GrCfg {
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-// x . (the row's 32 bf16 values in four 16-byte pieces of a swizzled panel row).
-__device__ __forceinline__ float row_dot32(const float (&x)[32], uint32_t panel, int row, int chunk0) {
+// x . (the row's 16 bf16 values in two 16-byte pieces of a swizzled panel row).
+__device__ __forceinline__ float row_dot16(const float (&x)[16], uint32_t panel, int row, int chunk0) {
     float2 d[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
+    for (int ch = 0; ch < 2; ++ch) {
         uint32_t a[4];
         ld_shared_v4(panel + sw128_off(row, chunk0 + ch), a[0], a[1], a[2], a[3]);
 #pragma unroll
@@ -1058,18 +1068,18 @@ __device__ __forceinline__ float row_dot32(const float (&x)[32], uint32_t panel,
 }
 
 // x *= f, and back to tensor memory.
-__device__ __forceinline__ void scale32(uint32_t taddr, float f, float (&x)[32]) {
-    uint32_t w[32];
+__device__ __forceinline__ void scale16(uint32_t taddr, float f, float (&x)[16]) {
+    uint32_t w[16];
     const float2 ff = make_float2(f, f);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
+    for (int i = 0; i < 16; i += 2) {
         const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), ff);
         x[i] = y.x;
         x[i + 1] = y.y;
         w[i] = __float_as_uint(y.x);
         w[i + 1] = __float_as_uint(y.y);
     }
-    tmem_st32(taddr, w);
+    tmem_st16(taddr, w);
 }
 
 // Start the TMA store of a staged [128][D] tile (one thread; its own bulk group).
@@ -1144,7 +1154,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                 for (int k = 0; k < 6; ++k) {
                     const int t = order[k];
-                    if (g >= Cfg::NS && !mbar_wait(empty(s, t), ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x800 + t))
+                    if (g >= Cfg::NS && !wait_one(empty(s, t), ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x800 + t))
                         return false;
                     if (t == Cfg::F_S || t == Cfg::F_E) {
                         mbar_arrive_expect_tx(full(s, t), Cfg::SB);
@@ -1192,7 +1202,7 @@ __global__ void __launch_bounds__(640, 1)
             constexpr uint32_t kIdW = idesc_bf16_f32(C, D, true, true);     // W K, W held transposed
             bool issued = false;
             auto wait = [&](int b, int64_t phase, unsigned where) {
-                return mbar_wait(&bar[b], static_cast<uint32_t>(phase & 1), abort_flag, tmo, where);
+                return wait_one(&bar[b], static_cast<uint32_t>(phase & 1), abort_flag, tmo, where);
             };
             walk([&](const GatedChunk& ch, int64_t, int64_t g) {
                 const int s = static_cast<int>(g % Cfg::NS);
@@ -1288,7 +1298,7 @@ __global__ void __launch_bounds__(640, 1)
             // (S: its tile was given back behind the last use of these decays' place.  V is waited for only where its
             // rows are zeroed: a full chunk's V may be given back, and loaded again, before this warp looks at it)
             for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_O, Cfg::F_S, Cfg::F_V})
-                if ((t != Cfg::F_V || ch.nv < C) && !mbar_wait_warp(full(s, t), ph, abort_flag, tmo, 0x820 + t)) return false;
+                if ((t != Cfg::F_V || ch.nv < C) && !wait_warp(full(s, t), ph, abort_flag, tmo, 0x820 + t)) return false;
             float4* o = reinterpret_cast<float4*>(smem + Cfg::OFF_G + (g & 1) * 4 * C * 4);
             o[lane] = make_float4(G[0], G[1], G[2], G[3]);
             o[32 + lane] = make_float4(ex2(G[0]), ex2(G[1]), ex2(G[2]), ex2(G[3]));
@@ -1302,7 +1312,7 @@ __global__ void __launch_bounds__(640, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
             // dv, the last result of the chunk
-            if (!mbar_wait_warp(&bar[Cfg::B_STAGED + 2], static_cast<uint32_t>(g & 1), abort_flag, tmo, 0x834)) return false;
+            if (!wait_warp(&bar[Cfg::B_STAGED + 2], static_cast<uint32_t>(g & 1), abort_flag, tmo, 0x834)) return false;
             if (lane == 0) {
                 if (ch.nv == C) {
                     store_tile<D>(&m.dv, smem + s * Cfg::STAGE + Cfg::O, ch);
@@ -1319,7 +1329,7 @@ __global__ void __launch_bounds__(640, 1)
             const int s = static_cast<int>(g % Cfg::NS);
             const uint32_t gp = static_cast<uint32_t>(g & 1);
             auto store = [&](int n, int tile, const CUtensorMap* map) {
-                if (!mbar_wait_warp(&bar[Cfg::B_STAGED + n], gp, abort_flag, tmo, 0x832 + n)) return false;
+                if (!wait_warp(&bar[Cfg::B_STAGED + n], gp, abort_flag, tmo, 0x832 + n)) return false;
                 if (lane == 0 && ch.nv == C) store_tile<D>(map, smem + s * Cfg::STAGE + tile * Cfg::TILE, ch);
                 return true;
             };
@@ -1331,7 +1341,7 @@ __global__ void __launch_bounds__(640, 1)
                 mbar_arrive(empty(s, Cfg::F_K));
             }
             __syncwarp();
-            if (!mbar_wait_warp(&bar[Cfg::B_SUMS], gp, abort_flag, tmo, 0x830)) return false;
+            if (!wait_warp(&bar[Cfg::B_SUMS], gp, abort_flag, tmo, 0x830)) return false;
             const float* es = reinterpret_cast<const float*>(smem + Cfg::OFF_ES);
             auto get = [&](int off, float (&x)[4]) {
                 const float4* a = reinterpret_cast<const float4*>(smem + off);
@@ -1384,7 +1394,7 @@ __global__ void __launch_bounds__(640, 1)
             const uint32_t ph = (g / Cfg::NS) & 1, gp = static_cast<uint32_t>(g & 1);
             const uint32_t st = sbase + s * Cfg::STAGE;
             auto wait = [&](int b, uint32_t parity, unsigned where) {
-                return mbar_wait_warp(&bar[b], parity, abort_flag, tmo, where);
+                return wait_warp(&bar[b], parity, abort_flag, tmo, where);
             };
             auto arrive = [&](int b) {
                 __syncwarp();
@@ -1404,45 +1414,36 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) pw[e] = ww[e] = 0u;
             } else {
-                const float Gj = G[row];
+                const float Gj = G[row], fj = ib > sub ? ex2(G[ib * 32 - 1] - Gj) : 0.f;
                 const uint32_t ta = tmem + Cfg::T0 + lanes + ib * 32, tb = tmem + Cfg::T1 + lanes + ib * 32;
-                if (ib > sub) {
-                    const float fj = ex2(G[ib * 32 - 1] - Gj);
 #pragma unroll
-                    for (int hb = 0; hb < 2; ++hb) {
-                        float a[16], b[16];
-                        ld16f2(ta + hb * 16, tb + hb * 16, a, b);
+                for (int hb = 0; hb < 2; ++hb) {
+                    float a[16], b[16];
+                    ld16f2(ta + hb * 16, tb + hb * 16, a, b);
+                    if (ib > sub) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float4 f = reinterpret_cast<const float4*>(F + ib * 32 + hb * 16)[e];
                             const float w[4] = {fj * f.x, fj * f.y, fj * f.z, fj * f.w};
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int c = 4 * e + 2 * h;
-                                pw[8 * hb + 2 * e + h] = pack_bf16x2(w[2 * h] * a[c], w[2 * h + 1] * a[c + 1]);
-                                ww[8 * hb + 2 * e + h] = pack_bf16x2(w[2 * h] * b[c], w[2 * h + 1] * b[c + 1]);
+                            for (int h = 0; h < 4; ++h) {
+                                a[4 * e + h] *= w[h];
+                                b[4 * e + h] *= w[h];
                             }
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float w = ex2(G[ib * 32 + hb * 16 + c] - Gj);
+                            const bool in = hb * 16 + c >= lane;
+                            a[c] = in ? w * a[c] : 0.f;
+                            b[c] = in ? w * b[c] : 0.f;
                         }
                     }
-                } else {
 #pragma unroll
-                    for (int hb = 0; hb < 2; ++hb) {
-                        float a[16], b[16];
-                        ld16f2(ta + hb * 16, tb + hb * 16, a, b);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float pv[2], wv[2];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int c = 2 * e + h;
-                                const bool in = hb * 16 + c >= lane;
-                                const float w = ex2(G[ib * 32 + hb * 16 + c] - Gj);
-                                pv[h] = in ? w * a[c] : 0.f;
-                                wv[h] = in ? w * b[c] : 0.f;
-                            }
-                            pw[8 * hb + e] = pack_bf16x2(pv[0], pv[1]);
-                            ww[8 * hb + e] = pack_bf16x2(wv[0], wv[1]);
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        pw[8 * hb + e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+                        ww[8 * hb + e] = pack_bf16x2(b[2 * e], b[2 * e + 1]);
                     }
                 }
             }
@@ -1469,11 +1470,16 @@ __global__ void __launch_bounds__(640, 1)
             // the sums of the chunk before are read
             if (g >= 1 && !wait(Cfg::B_SUMFREE, gp ^ 1u, 0x841)) return false;
             if (wide) {
-                float x[32], y[32];
-                ld32f2(tmem + Cfg::T2 + dcol, tmem + Cfg::T3 + dcol, x, y);
-                scale32(tmem + Cfg::T2 + dcol, Pre[row], x);
-                scale32(tmem + Cfg::T3 + dcol, Suf[row], y);
-                cj[quarter * C + row] = row_dot32(y, st + Cfg::K + pan * kPanel, row, ch0);
+                float dot = 0.f;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float x[16], y[16];
+                    ld16f2(tmem + Cfg::T2 + dcol + h * 16, tmem + Cfg::T3 + dcol + h * 16, x, y);
+                    scale16(tmem + Cfg::T2 + dcol + h * 16, Pre[row], x);
+                    scale16(tmem + Cfg::T3 + dcol + h * 16, Suf[row], y);
+                    dot += row_dot16(y, st + Cfg::K + pan * kPanel, row, ch0 + 2 * h);
+                }
+                cj[quarter * C + row] = dot;
             }
             tmem_wait_st();
             tc_fence_before();
@@ -1481,9 +1487,12 @@ __global__ void __launch_bounds__(640, 1)
             if (!wait(Cfg::B_Z, gp, 0x847)) return false;
             tc_fence_after();
             if (wide) {
-                float x[32];
-                ld32f(tmem + Cfg::T1 + dcol, x);
-                scale32(tmem + Cfg::T1 + dcol, Suf[row], x);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float x[16];
+                    ld16f(tmem + Cfg::T1 + dcol + h * 16, x);
+                    scale16(tmem + Cfg::T1 + dcol + h * 16, Suf[row], x);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -1511,58 +1520,39 @@ __global__ void __launch_bounds__(640, 1)
                 }
             }
             // results: into the tile of q, k or dO, whose last reader is done; returns the dot product with what it held
-            auto result = [&](const float (&x)[32], int tile, void* dst, bool dot) -> float {
-                const uint32_t panel = st + tile * Cfg::TILE + pan * kPanel;
-                const float sum = dot ? row_dot32(x, panel, row, ch0) : 0.f;
-                if (ch.nv == C) {
-                    put_row32(panel, row, ch0, x);
+            auto result = [&](int tm, int n, int tile, void* dst, bool dot) -> float {
+                float sum = 0.f;
+                if (wide) {
+                    const uint32_t panel = st + tile * Cfg::TILE + pan * kPanel;
+                    uint16_t* out = static_cast<uint16_t*>(dst) + (ch.row0 + row) * D + quarter * 32;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        float x[16];
+                        ld16f(tmem + tm + dcol + h * 16, x);
+                        if (dot) sum += row_dot16(x, panel, row, ch0 + 2 * h);
+                        if (ch.nv == C)
+                            put_row16(panel, row, ch0 + 2 * h, x);
+                        else if (row < ch.nv)
+                            put_row16(out + h * 16, x);
+                    }
                     fence_proxy_async_smem();
-                } else if (row < ch.nv) {
-                    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + (ch.row0 + row) * D + quarter * 32);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        out[e] = make_uint4(pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
-                                            pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
                 }
+                tc_fence_before();
+                arrive(Cfg::B_FREE + n);
+                if (wide && lane == 0) mbar_arrive(&bar[Cfg::B_STAGED + n]);
                 return sum;
             };
             if (!wait(Cfg::B_DK, gp, 0x850)) return false;
             tc_fence_after();
             float u = 0.f;
-            {
-                auto read = [&] {
-                    tc_fence_before();
-                    arrive(Cfg::B_FREE + 0);
-                    if (lane == 0) mbar_arrive(&bar[Cfg::B_FREE + 1]);
-                };
-                if (!wide) {
-                    read();
-                } else {
-                    float x[32], y[32];
-                    ld32f2(tmem + Cfg::T2 + dcol, tmem + Cfg::T3 + dcol, x, y);
-                    read();
-                    u = result(x, Cfg::F_Q, p.dq, true);
-                    arrive(Cfg::B_STAGED + 0);
-                    u -= result(y, Cfg::F_K, p.dk_, true);
-                    arrive(Cfg::B_STAGED + 1);
-                }
-            }
+#pragma unroll 1
+            for (int n = 0; n < 2; ++n)
+                u += n == 0 ? result(Cfg::T2, 0, Cfg::F_Q, p.dq, true) : -result(Cfg::T3, 1, Cfg::F_K, p.dk_, true);
             if (wide) us[quarter * C + row] = u;
             arrive(Cfg::B_SUMS);
             if (!wait(Cfg::B_DV, gp, 0x851)) return false;
             tc_fence_after();
-            {
-                if (!wide) {
-                    arrive(Cfg::B_FREE + 2);
-                } else {
-                    float x[32];
-                    ld32f(tmem + Cfg::T1 + dcol, x);
-                    tc_fence_before();
-                    arrive(Cfg::B_FREE + 2);
-                    result(x, Cfg::F_O, p.dv_, false);
-                    arrive(Cfg::B_STAGED + 2);
-                }
-            }
+            result(Cfg::T1, 2, Cfg::F_O, p.dv_, false);
             return true;
         });
     }
