@@ -60,8 +60,8 @@ struct GatedProblem {
     const int32_t* choff;  // packed: chunks before sequence n, num_seqs + 1 entries
     const int32_t* order;  // packed: the sequences, longest first (nullptr: in their order)
     int64_t nc;            // chunk slots per group
-    // Tensor-core prefill: [0] chunks published, [1] chunks taken, [2] chunks per group (packed), then from kQueueHead
-    // on the published slots, plus one.  All zero at the start but [2].
+    // Tensor-core prefill: [0] chunks published, [1] chunks taken, [2] chunks per group (packed), [3] units claimed, then
+    // from kQueueHead on the published slots, plus one.  All zero at the start but [2].
     unsigned int* queue;
     void* s_states;        // state at each chunk's start
     void* e_states;        // gradient of the state at each chunk's end

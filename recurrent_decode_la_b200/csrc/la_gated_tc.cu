@@ -204,8 +204,9 @@ __device__ __forceinline__ uint32_t tile_k(uint32_t tile, int ks, uint32_t panel
 // ---------------------------------------------------------------------------
 // States.  A work item is a unit, forward: X = K, Y = V; for the gradient also
 // in reverse: X = Q, Y = dO.  The units of packed input come longest first
-// (p.order), dealt to the CTAs in turn and back, so that no CTA gets the longer
-// item of every round.  Per chunk
+// (p.order): for the gradient dealt to the CTAs in turn and back, so that no CTA
+// gets the longer item of every round; in the prefill claimed from a counter.
+// Per chunk
 //     U = X'^T Y (X' = the decayed rows, as the sum of three bf16 numbers),
 //     S = gamma S + U.
 //   warp 0       TMA producer        warp 1  MMA issuer
@@ -234,9 +235,12 @@ struct StCfg {
     static constexpr int OFF_W = OFF_SB + SB;
     static constexpr int NW = 2;            // sets of decays, each [3][128] bf16: w = w0 + w1 + w2
     static constexpr int OFF_GAM = OFF_W + NW * 3 * C * 2;
-    static constexpr int OFF_BAR = OFF_GAM + kGam * 4;
+    static constexpr int kItems = 4;  // claimed items that the roles may be apart
+    static constexpr int OFF_ITEMS = OFF_GAM + kGam * 4;
+    static constexpr int OFF_BAR = OFF_ITEMS + kItems * 4;
     static constexpr int B_FULL = 0, B_EMPTY = NS, B_GFULL = 2 * NS, B_SCALED = 3 * NS, B_UFULL = 4 * NS,
-                         B_UEMPTY = 4 * NS + NU, B_DONE = 4 * NS + 2 * NU, B_LOEMPTY = B_DONE + 1, NBAR = B_DONE + 1 + NL;
+                         B_UEMPTY = 4 * NS + NU, B_DONE = 4 * NS + 2 * NU, B_LOEMPTY = B_DONE + 1, B_IFULL = B_LOEMPTY + NL,
+                         B_IEMPTY = B_IFULL + kItems, NBAR = B_IEMPTY + kItems;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     // columns of part k of buffer l (TS)
@@ -271,27 +275,60 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         }
         mbar_init(&bar[Cfg::B_DONE], 1);
         for (int l = 0; l < Cfg::NL; ++l) mbar_init(&bar[Cfg::B_LOEMPTY + l], 1);
+        for (int r = 0; r < Cfg::kItems; ++r) {
+            mbar_init(&bar[Cfg::B_IFULL + r], 1);
+            mbar_init(&bar[Cfg::B_IEMPTY + r], 3 + 8 + 4 * Cfg::NPAN);
+        }
         *abort_flag = 0;
         *stored = 0;
         fence_barrier_init();
     }
     __syncthreads();
 
+    // Claimed items (prefill): the producer takes them from the counter and publishes them to the other roles, whose
+    // threads are a whole warp or its lane 0 alone.
+    enum Role { kProducer, kLane, kWarp };
+    volatile int* claimed = reinterpret_cast<volatile int*>(smem + Cfg::OFF_ITEMS);
+    auto claim = [&](Role role, int64_t k, int64_t& i) -> bool {
+        const int r = static_cast<int>(k % Cfg::kItems);
+        const uint32_t ph = static_cast<uint32_t>(k / Cfg::kItems) & 1;
+        if (role == kProducer) {
+            const unsigned int at = atomicAdd(&p.queue[3], 1u);
+            i = at < n_items ? static_cast<int64_t>(at) : -1;
+            if (k >= Cfg::kItems && !wait_one(&bar[Cfg::B_IEMPTY + r], ph ^ 1u, abort_flag, tmo, 0x660)) return false;
+            claimed[r] = static_cast<int>(i);
+            mbar_arrive(&bar[Cfg::B_IFULL + r]);
+            return true;
+        }
+        if (!(role == kWarp ? wait_warp(&bar[Cfg::B_IFULL + r], ph, abort_flag, tmo, 0x661)
+                            : wait_one(&bar[Cfg::B_IFULL + r], ph, abort_flag, tmo, 0x662)))
+            return false;
+        i = claimed[r];
+        if (role == kWarp) __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[Cfg::B_IEMPTY + r]);
+        return true;
+    };
     // Calls f(unit, its state, reverse) for every item of this CTA until f gives up.
-    auto items = [&](auto&& f) {
+    auto items = [&](Role role, auto&& f) {
         for (int64_t k = 0;; ++k) {
-            const int64_t i = k * workers + (k & 1 ? workers - 1 - worker : worker);
-            if (k * workers >= n_items) return true;
-            if (i >= n_items) continue;
+            int64_t i;
+            if (p.queue != nullptr) {
+                if (!claim(role, k, i)) return false;
+                if (i < 0) return true;
+            } else {
+                i = k * workers + (k & 1 ? workers - 1 - worker : worker);
+                if (k * workers >= n_items) return true;
+                if (i >= n_items) continue;
+            }
             int64_t u = grad ? i >> 1 : i;
             if (p.order != nullptr) u = static_cast<int64_t>(p.order[u / p.H]) * p.H + u % p.H;
             if (!f(gated_unit(p, u), u, grad && (i & 1))) return false;
         }
     };
     // Calls f(unit, reverse, chunk, rows of it, chunks before it) for every chunk of them.
-    auto walk = [&](auto&& f) -> bool {
+    auto walk = [&](Role role, auto&& f) -> bool {
         int64_t g = 0;
-        return items([&](const GatedUnit& un, int64_t, bool rev) {
+        return items(role, [&](const GatedUnit& un, int64_t, bool rev) {
             const int nch = (un.len + C - 1) / C;
             for (int cc = 0; cc < nch; ++cc, ++g) {
                 const int c = rev ? nch - 1 - cc : cc;
@@ -309,7 +346,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 group = static_cast<int>(un.row0 / p.rows);
                 row = static_cast<int>(r - group * p.rows);
             };
-            const bool ok = walk([&](const GatedUnit& un, bool rev, int c, int, int64_t g) {
+            const bool ok = walk(kProducer, [&](const GatedUnit& un, bool rev, int c, int, int64_t g) {
                 const int s = static_cast<int>(g % Cfg::NS);
                 if (g >= Cfg::NS &&
                     !wait_one(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x600 + s))
@@ -345,7 +382,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         if (lane == 0) {
             constexpr uint32_t kId = idesc_bf16_f32(D, D, !Cfg::TS, true);
             bool issued = false;
-            walk([&](const GatedUnit&, bool, int, int, int64_t g) {
+            walk(kLane, [&](const GatedUnit&, bool, int, int, int64_t g) {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g % Cfg::NU), l = static_cast<int>(g % Cfg::NL);
                 if (!wait_one(&bar[Cfg::B_SCALED + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x610 + s)) return false;
                 if (g >= Cfg::NU &&
@@ -382,7 +419,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         }
         __syncwarp();
     } else if (warp == 2) {
-        walk([&](const GatedUnit& un, bool rev, int c, int nv, int64_t g) {
+        walk(kWarp, [&](const GatedUnit& un, bool rev, int c, int nv, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
             float x[4], w[4], all;
             load_gates(p, un.row0 + static_cast<int64_t>(c) * C, nv, x);
@@ -415,7 +452,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
     } else if (warp == 3) {
         // publish a chunk's slot once every part of its state is in global memory
         if (lane == 0 && p.queue != nullptr) {
-            walk([&](const GatedUnit& un, bool, int c, int, int64_t g) {
+            walk(kLane, [&](const GatedUnit& un, bool, int c, int, int64_t g) {
                 const unsigned int want = static_cast<unsigned int>(g + 1) * (4 * Cfg::NPAN);
                 if (!wait_until(tmo, abort_flag, 0x650, [&] {
                         unsigned int have;
@@ -433,7 +470,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {
-        walk([&](const GatedUnit&, bool, int, int nv, int64_t g) {
+        walk(kWarp, [&](const GatedUnit&, bool, int, int nv, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
             const uint32_t ph = (g / Cfg::NS) & 1;
             if (!wait_warp(&bar[Cfg::B_GFULL + s], ph, abort_flag, tmo, 0x630 + s)) return false;
@@ -549,7 +586,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         auto count_stored = [&] {
             asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(stored)) : "memory");
         };
-        items([&](const GatedUnit& un, int64_t u, bool rev) {
+        items(kWarp, [&](const GatedUnit& un, int64_t u, bool rev) {
             const int nch = (un.len + C - 1) / C;
             if (nch == 0) return true;
             const float* in = rev ? p.dstate : (p.state ? p.state : p.s0);
@@ -984,8 +1021,9 @@ __global__ void __launch_bounds__(640, 1)
 
 // The prefill in one launch: the first n_state CTAs make the states and publish each chunk as its state is stored; the
 // others, and those when they are done, take the chunks in that order.  So K, V and the states come from L2 the second
-// time, and the serial phase of few long sequences overlaps the other.  Only the later CTAs wait, for ones that the
-// device starts before them.
+// time, and the serial phase of few long sequences overlaps the other.  A CTA waits only for units that CTAs already
+// running have claimed: one of the first takes chunks only when every unit is claimed, and the device starts the others
+// after them.  So it does not matter how many of the CTAs are on the device at once.
 template <int D>
 __global__ void __launch_bounds__(640, 1)
     gated_prefill_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items, int n_state) {
@@ -1586,9 +1624,10 @@ cudaError_t prefill_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cu
     static PerDeviceOnce once;
     cudaError_t e = raise_smem(once, gated_prefill_tc_kernel<D>, kSmem);
     if (e != cudaSuccess) return e;
-    // A chunk's state takes about three quarters of the time of its output: as many CTAs as make the states in the
-    // fewest rounds on 45 % of the device.
-    const int most = std::max(1, num_sms * 45 / 100);
+    // As many CTAs as make the states in the fewest rounds on three quarters of the device.  Measured at 30, 45, 60, 75,
+    // 90 and 100 %: B8 H16 T8192 466 369 369 369 382 382 us, B16 H32 T256 137 102 86 80 82 81, B4 H32 T512 59 46 46 46 43
+    // 43, 24 packed sequences 288 233 239 225 231 209 (all d 128).
+    const int most = std::max(1, num_sms * 75 / 100);
     const int64_t rounds = (p.n_units + most - 1) / most;
     const int n_state = static_cast<int>((p.n_units + rounds - 1) / rounds);
     const int64_t slots = p.groups * p.nc;
