@@ -63,6 +63,14 @@ struct GatedProblem {
     // Tensor-core prefill: [0] chunks published, [1] chunks taken, [2] chunks per group (packed), [3] units claimed, then
     // from kQueueHead on the published slots, plus one.  All zero at the start but [2].
     unsigned int* queue;
+    // Segments of a unit's walk (few long units): segs runs of seg_chunks chunks, each walked by itself.  A first pass
+    // (sums) makes what each adds to a state of zero, with its decay; their prefix gives each one's start; the second
+    // pass goes on from there.  seg_states [directions][units][segs][d_k][d_v], seg_decays [directions][units][segs].
+    int segs;
+    int seg_chunks;
+    bool sums;
+    float* seg_states;
+    float* seg_decays;
     void* s_states;        // state at each chunk's start
     void* e_states;        // gradient of the state at each chunk's end
     uint64_t timeout_ns;
@@ -129,6 +137,10 @@ constexpr int kMaxGatedOrder = 1024;
 cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, int C, int32_t* choff, int32_t* order,
                                  int64_t nc, unsigned int* used, cudaStream_t s);
 
+// seg_states[..][s] = the start of segment s, from S_0 (dS_T) and the sums of
+// the segments before it.
+cudaError_t launch_segment_starts(const GatedProblem& p, int chunk, bool grad, cudaStream_t s);
+
 // CUDA-core kernels: fp32 throughout, fp32 chunk states, any d_k, d_v <= 128.
 constexpr int kGatedSimtChunk = 32;
 cudaError_t launch_gated_states_simt(const GatedProblem& p, bool grad, cudaStream_t s);
@@ -144,8 +156,8 @@ struct GatedMaps {
     CUtensorMap o;                  // stores: 64 columns x 32 rows
     CUtensorMap dq, dk, dv;         // stores: 64 columns x 128 rows
 };
-// States at the chunk starts and gradients at the chunk ends (for the gradient).
-cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);
+// States at the chunk starts and, for the gradient, gradients at the chunk ends; or the segments' sums.
+cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s);
 // The whole prefill.
 cudaError_t launch_gated_prefill_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);
 cudaError_t launch_gated_grad_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s);

@@ -3,6 +3,8 @@
 // workspace layout and launches.  Host code only.
 #include <stdio.h>
 
+#include <algorithm>
+
 #include "../../include/linattn.h"
 #include "la_gated.h"
 #include "la_internal.h"
@@ -28,6 +30,10 @@ Kernel choose(la_dtype dtype, int64_t max_tokens, int dk, int dv, bool grad) {
     return kSimt;
 }
 
+// CTAs that the split of few units aims at: one a SM of the part this is written for.  Not the current device's count: the
+// workspace that a caller asked for has to fit on any.
+constexpr int64_t kPlanSms = 148;
+
 // Chunk states in the workspace: packed, first the chunk offsets (num_seqs + 1
 // int32) and the sequences by length (num_seqs int32); for the tensor-core prefill
 // the queue of published chunks; then one state per chunk slot, and for the gradient one gradient of
@@ -35,7 +41,8 @@ Kernel choose(la_dtype dtype, int64_t max_tokens, int dk, int dv, bool grad) {
 struct Layout {
     int chunk = 0;
     int64_t nc = 0;
-    size_t queue = 0, s = 0, e = 0, bytes = 0;
+    int segs = 1, seg_chunks = 0;
+    size_t queue = 0, seg = 0, s = 0, e = 0, bytes = 0;
 };
 Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs, bool grad) {
     Layout w;
@@ -44,8 +51,23 @@ Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs
     // a packed sequence begins a chunk of its own
     w.nc = num_seqs > 0 ? T / w.chunk + num_seqs : (T + w.chunk - 1) / w.chunk;
     const size_t states = up256(static_cast<size_t>(groups) * w.nc * dk * dv * (kind == kTc ? 2 : 4));
+    // Few long units: the walk is cut into segments, walked twice (their sums, then their chunks), so that more of the
+    // device works on it, where that leaves at most half of it one behind the other (with three segments 32 heads of
+    // 4096 tokens took 118 us, unsplit 107).  From four tensor-core chunks a segment, or two of the CUDA cores: below,
+    // the second walk costs what it saves (two tensor-core chunks, 2 heads of 1000 tokens: 43 us, unsplit 35).  Unsplit
+    // and split: 8 heads of 16384 tokens 270 and 114 us, their gradient 310 and 183; 8 heads of 4000 83 and 59; fp32, 4
+    // heads of 8000 180 and 75, their gradient 751 and 242.
+    const int64_t units = groups * std::max(1, num_seqs), nch = (T + w.chunk - 1) / w.chunk;
+    const int64_t ctas = units * (grad ? 2 : 1) * (kind == kTc ? 1 : (dv + 31) / 32);
+    const int64_t room = kind == kSimt ? 2 * kPlanSms : grad ? kPlanSms : kPlanSms * 3 / 4;
+    int64_t segs = std::min<int64_t>({room / ctas, nch / (kind == kTc ? 4 : 2), 64});
+    if (segs < 4) segs = 1;
+    w.seg_chunks = static_cast<int>((nch + segs - 1) / segs);
+    w.segs = static_cast<int>((nch + w.seg_chunks - 1) / w.seg_chunks);
     w.queue = num_seqs > 0 ? up256((2 * static_cast<size_t>(num_seqs) + 1) * 4) : 0;
-    w.s = w.queue + (kind == kTc && !grad ? up256((static_cast<size_t>(groups) * w.nc + kQueueHead) * 4) : 0);
+    w.seg = w.queue + (kind == kTc && !grad ? up256((static_cast<size_t>(groups) * w.nc + kQueueHead) * 4) : 0);
+    w.s = w.seg;
+    if (w.segs > 1) w.s += up256(static_cast<size_t>(units) * (grad ? 2 : 1) * w.segs * (static_cast<size_t>(dk) * dv + 1) * 4);
     w.e = w.s + states;
     w.bytes = w.e + (grad ? states : 0);
     return w;
@@ -83,7 +105,7 @@ la_status sizes(GatedProblem& p, la_dtype dtype, int B, int H, int64_t T, int dk
     return LA_OK;
 }
 
-la_status place(GatedProblem& p, const Layout& w, void* workspace, size_t bytes) {
+la_status place(GatedProblem& p, const Layout& w, bool grad, void* workspace, size_t bytes) {
     if (p.groups * w.nc > 0x7fffffffLL || p.n_units > (1 << 28)) return refuse(LA_ERR_UNSUPPORTED, "too many chunks for one call");
     if (!workspace || bytes < w.bytes || !aligned16(workspace)) {
         char why[128];
@@ -93,8 +115,14 @@ la_status place(GatedProblem& p, const Layout& w, void* workspace, size_t bytes)
     }
     char* base = static_cast<char*>(workspace);
     p.nc = w.nc;
+    p.segs = w.segs;
+    p.seg_chunks = w.seg_chunks;
     p.choff = p.cu ? reinterpret_cast<const int32_t*>(base) : nullptr;
     p.order = p.cu && p.num_seqs <= kMaxGatedOrder ? p.choff + p.num_seqs + 1 : nullptr;
+    if (w.segs > 1) {
+        p.seg_states = reinterpret_cast<float*>(base + w.seg);
+        p.seg_decays = p.seg_states + static_cast<size_t>(p.n_units) * (grad ? 2 : 1) * w.segs * p.dk * p.dv;
+    }
     p.s_states = base + w.s;
     p.e_states = base + w.e;
     return LA_OK;
@@ -104,6 +132,17 @@ cudaError_t chunk_offsets(const GatedProblem& p, const Layout& w, cudaStream_t s
     if (!p.cu) return cudaSuccess;
     return launch_chunk_offsets(p.cu, p.num_seqs, p.rows, w.chunk, const_cast<int32_t*>(p.choff), const_cast<int32_t*>(p.order), w.nc,
                                 p.queue ? p.queue + 2 : nullptr, s);
+}
+
+// Where the walk is cut: every segment's sum, then its start.
+template <typename F>
+cudaError_t segment_starts(const GatedProblem& p, const Layout& w, bool grad, F&& states, cudaStream_t s) {
+    if (p.segs == 1) return cudaSuccess;
+    GatedProblem q = p;
+    q.sums = true;
+    q.queue = nullptr;
+    const cudaError_t e = states(q);
+    return e != cudaSuccess ? e : launch_segment_starts(p, w.chunk, grad, s);
 }
 
 // The tensor maps of the tensor-core kernels (every tensor 16-byte aligned).
@@ -174,18 +213,23 @@ la_status la_gated_prefill(const void* q, const void* k, const void* v, const vo
         return e == cudaSuccess ? LA_OK : fail(e);
     }
     const Layout w = plan(kind, p.groups, T, d_k, d_v, p.num_seqs, false);
-    if ((st = place(p, w, workspace, workspace_bytes)) != LA_OK) return st;
+    if ((st = place(p, w, false, workspace, workspace_bytes)) != LA_OK) return st;
     p.q = q; p.k = k; p.v = v; p.g = g; p.o = o; p.state = state;
     if (kind == kTc) {
         GatedMaps m = {};
         if ((st = maps(m, p, false)) != LA_OK) return st;
         p.queue = reinterpret_cast<unsigned int*>(static_cast<char*>(workspace) + w.queue);
-        e = cudaMemsetAsync(p.queue, 0, w.s - w.queue, s);
+        const int sms = current_sm_count();
+        e = cudaMemsetAsync(p.queue, 0, w.seg - w.queue, s);
         if (e == cudaSuccess) e = chunk_offsets(p, w, s);
-        if (e == cudaSuccess) e = launch_gated_prefill_tc(p, m, current_sm_count(), s);
+        if (e == cudaSuccess)
+            e = segment_starts(p, w, false, [&](const GatedProblem& q) { return launch_gated_states_tc(q, m, false, sms, s); }, s);
+        if (e == cudaSuccess) e = launch_gated_prefill_tc(p, m, sms, s);
         return e == cudaSuccess ? LA_OK : fail(e);
     }
     e = chunk_offsets(p, w, s);
+    if (e == cudaSuccess)
+        e = segment_starts(p, w, false, [&](const GatedProblem& q) { return launch_gated_states_simt(q, false, s); }, s);
     if (e == cudaSuccess) e = launch_gated_states_simt(p, false, s);
     if (e == cudaSuccess) e = launch_gated_out_simt(p, s);
     return e == cudaSuccess ? LA_OK : fail(e);
@@ -203,7 +247,7 @@ la_status la_gated_prefill_backward(const void* q, const void* k, const void* v,
         return refuse(LA_ERR_INVALID_ARG, "a tensor is NULL");
     const Kernel kind = choose(dtype, 0, d_k, d_v, true);
     const Layout w = plan(kind, p.groups, T, d_k, d_v, p.num_seqs, true);
-    if ((st = place(p, w, workspace, workspace_bytes)) != LA_OK) return st;
+    if ((st = place(p, w, true, workspace, workspace_bytes)) != LA_OK) return st;
     p.q = q; p.k = k; p.v = v; p.g = g;
     p.s0 = state0;
     p.d_o = d_o;
@@ -216,11 +260,15 @@ la_status la_gated_prefill_backward(const void* q, const void* k, const void* v,
         if ((st = maps(m, p, true)) != LA_OK) return st;
         const int sms = current_sm_count();
         e = chunk_offsets(p, w, s);
-        if (e == cudaSuccess) e = launch_gated_states_tc(p, m, sms, s);
+        if (e == cudaSuccess)
+            e = segment_starts(p, w, true, [&](const GatedProblem& q) { return launch_gated_states_tc(q, m, true, sms, s); }, s);
+        if (e == cudaSuccess) e = launch_gated_states_tc(p, m, true, sms, s);
         if (e == cudaSuccess) e = launch_gated_grad_tc(p, m, sms, s);
         return e == cudaSuccess ? LA_OK : fail(e);
     }
     e = chunk_offsets(p, w, s);
+    if (e == cudaSuccess)
+        e = segment_starts(p, w, true, [&](const GatedProblem& q) { return launch_gated_states_simt(q, true, s); }, s);
     if (e == cudaSuccess) e = launch_gated_states_simt(p, true, s);
     if (e == cudaSuccess) e = launch_gated_grad_simt(p, s);
     return e == cudaSuccess ? LA_OK : fail(e);

@@ -160,8 +160,10 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
     __shared__ float Y[C][36];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x;
-    const bool rev = blockIdx.x / col_blocks >= p.n_units;
-    const int64_t u = blockIdx.x / col_blocks - (rev ? p.n_units : 0);
+    const int64_t item = blockIdx.x / col_blocks;  // [direction][unit][segment]
+    const int seg = static_cast<int>(item % p.segs);
+    const bool rev = item / p.segs >= p.n_units;
+    const int64_t u = item / p.segs - (rev ? p.n_units : 0);
     const int c0 = static_cast<int>(blockIdx.x % col_blocks) * 32;
     const GatedUnit un = gated_unit(p, u);
     if (un.len == 0) return;
@@ -171,7 +173,15 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
     const float* in = rev ? p.dstate + u * usz : (p.state ? p.state + u * usz : (p.s0 ? p.s0 + u * usz : nullptr));
     float* out = rev ? p.dstate + u * usz : (p.state ? p.state + u * usz : nullptr);
     float* slots = static_cast<float*>(rev ? p.e_states : p.s_states);
-    float S[4][4];
+    const int nch = (un.len + C - 1) / C;
+    const int cc0 = seg * p.seg_chunks, cc1 = min(nch, cc0 + p.seg_chunks);
+    if (cc0 >= cc1 || (p.sums && cc1 == nch)) return;  // (nothing starts from the last one's sum)
+    if (p.segs > 1) {
+        float* start = p.seg_states + item * usz;
+        in = p.sums ? nullptr : start;
+        out = p.sums ? start : (cc1 == nch ? out : nullptr);
+    }
+    float S[4][4], whole = 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -179,7 +189,6 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
             S[i][m] = (in && r0 + i < dk && n0 + m < dv) ? in[(r0 + i) * dv + n0 + m] : 0.f;
     const T* xs = static_cast<const T*>(rev ? p.q : p.k);
     const T* ys = static_cast<const T*>(rev ? p.d_o : p.v);
-    const int nch = (un.len + C - 1) / C;
     auto chunk = [&](int cc) { return rev ? nch - 1 - cc : cc; };
     const int xc = tid & 127, xr = tid >> 7, yc = tid & 31, yr = tid >> 5;
     float xv[C / 2], yv[C / 8], gv;
@@ -198,8 +207,8 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
         }
         gv = load_gate<T>(p, row0, nv);
     };
-    fetch(0);
-    for (int cc = 0; cc < nch; ++cc) {
+    fetch(cc0);
+    for (int cc = cc0; cc < cc1; ++cc) {
         const int c = chunk(cc), nv = min(C, un.len - c * C);
         const double G = gate_scan(gv), all = __shfl_sync(0xffffffffu, G, 31);
         const float wt = decay(rev ? G : all - G), gamma = decay(all);  // of token `lane`
@@ -209,13 +218,14 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
 #pragma unroll
         for (int i = 0; i < C / 8; ++i) Y[yr + 8 * i][yc] = yv[i] * __shfl_sync(0xffffffffu, wt, yr + 8 * i);
         __syncthreads();
-        if (cc + 1 < nch) fetch(cc + 1);
+        if (cc + 1 < cc1) fetch(cc + 1);
+        whole *= gamma;
         float* slot = slots + (un.slot0 + c) * usz;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                if (r0 + i < dk && n0 + m < dv) slot[(r0 + i) * dv + n0 + m] = S[i][m];
+                if (!p.sums && r0 + i < dk && n0 + m < dv) slot[(r0 + i) * dv + n0 + m] = S[i][m];
                 S[i][m] *= gamma;
             }
 #pragma unroll 8
@@ -229,6 +239,7 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
                 for (int m = 0; m < 4; ++m) S[i][m] = fmaf(xa[i], ya[m], S[i][m]);
         }
     }
+    if (p.sums && blockIdx.x % col_blocks == 0 && tid == 0) p.seg_decays[item] = whole;
     if (out) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -463,6 +474,27 @@ __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __re
     }
 }
 
+// One thread per element of a unit's state: walks the unit's segments.
+__global__ void __launch_bounds__(256) segment_starts_kernel(const GatedProblem p, int chunk, int usz) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int per = (usz + 255) / 256;
+    const int64_t du = blockIdx.x / per;  // [direction][unit]
+    const int e = static_cast<int>(blockIdx.x % per) * 256 + threadIdx.x;
+    if (e >= usz) return;
+    const bool rev = du >= p.n_units;
+    const int64_t u = du - (rev ? p.n_units : 0);
+    const int nch = (gated_unit(p, u).len + chunk - 1) / chunk;
+    const float* in = rev ? p.dstate : (p.state ? p.state : p.s0);
+    float cur = in ? in[u * usz + e] : 0.f;
+    for (int s = 0; s * p.seg_chunks < nch; ++s) {
+        float* at = p.seg_states + (du * p.segs + s) * usz + e;
+        const bool last = (s + 1) * p.seg_chunks >= nch;
+        const float add = last ? 0.f : *at, decays = last ? 0.f : p.seg_decays[du * p.segs + s];
+        *at = cur;
+        cur = fmaf(decays, cur, add);
+    }
+}
+
 template <typename F>
 cudaError_t launch_chunks(PerDeviceOnce& once, F kern, int smem, const GatedProblem& p, cudaStream_t s) {
     const cudaError_t e =
@@ -498,9 +530,16 @@ cudaError_t launch_chunk_offsets(const int32_t* cu, int num_seqs, int64_t rows, 
     return launch_pdl(chunk_offsets_kernel, dim3(1), dim3(1024), 0, s, cu, num_seqs, rows, chunk, choff, order, nc, used);
 }
 
+cudaError_t launch_segment_starts(const GatedProblem& p, int chunk, bool grad, cudaStream_t s) {
+    const int usz = p.dk * p.dv;
+    const int64_t grid = p.n_units * (grad ? 2 : 1) * ((usz + 255) / 256);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch_pdl(segment_starts_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, p, chunk, usz);
+}
+
 cudaError_t launch_gated_states_simt(const GatedProblem& p, bool grad, cudaStream_t s) {
     const int cb = (p.dv + 31) / 32;
-    const int64_t grid = p.n_units * cb * (grad ? 2 : 1);
+    const int64_t grid = p.n_units * p.segs * cb * (grad ? 2 : 1);
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     const auto kern = p.dtype ? gated_states_simt_kernel<__nv_bfloat16> : gated_states_simt_kernel<float>;
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, p, cb);

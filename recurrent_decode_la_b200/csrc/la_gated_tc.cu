@@ -45,34 +45,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-#ifndef NSLEEP
-#define NSLEEP 32
-#endif
-// mbar_wait with a pause between polls.  Twenty warps share an SM's issue slots here, and a warp that polls without pause
-// takes them from those that compute: the scores of a block took ten clocks an instruction.
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns,
-                                         unsigned int where) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (NSLEEP) __nanosleep(NSLEEP);
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort) return false;
-            if (globaltimer_ns() - t0 > timeout_ns) {
-                record_timeout(where);
-                *abort = 1;
-                return false;
-            }
-        }
-    }
-}
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns,
-                                          unsigned int where) {
-    const bool ok = wait_one(bar, parity, abort, timeout_ns, where);
-    return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;
-}
-
 // Poll until f() holds; gives up like mbar_wait.
 template <typename F>
 __device__ __forceinline__ bool wait_until(uint64_t timeout_ns, volatile int* abort, unsigned int where, F&& f) {
@@ -152,8 +124,8 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int nv) {
     }
 }
 
-// The kernels below work on accumulator rows 16 columns at a time, in loops that are kept rolled: twenty warps in different
-// roles share the instruction cache, and with whole rows unrolled a warp waited for instructions ten clocks each.
+// The kernels below work on accumulator rows 16 columns at a time in loops that are kept rolled: no slower than whole rows
+// unrolled (the gradient up to 3 % faster), and twenty warps in different roles share the instruction cache.
 
 // 16 fp32 values of a row -> bf16, two 16-byte pieces of a 128-byte swizzled panel row.
 __device__ __forceinline__ void put_row16(uint32_t panel, int row, int chunk0, const float (&x)[16]) {
@@ -202,8 +174,8 @@ __device__ __forceinline__ uint32_t tile_k(uint32_t tile, int ks, uint32_t panel
 }
 
 // ---------------------------------------------------------------------------
-// States.  A work item is a unit, forward: X = K, Y = V; for the gradient also
-// in reverse: X = Q, Y = dO.  The units of packed input come longest first
+// States.  A work item is a segment of a unit (mostly all of it), forward: X = K,
+// Y = V; for the gradient also in reverse: X = Q, Y = dO.  The units of packed input come longest first
 // (p.order): for the gradient dealt to the CTAs in turn and back, so that no CTA
 // gets the longer item of every round; in the prefill claimed from a counter.
 // Per chunk
@@ -295,20 +267,21 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         if (role == kProducer) {
             const unsigned int at = atomicAdd(&p.queue[3], 1u);
             i = at < n_items ? static_cast<int64_t>(at) : -1;
-            if (k >= Cfg::kItems && !wait_one(&bar[Cfg::B_IEMPTY + r], ph ^ 1u, abort_flag, tmo, 0x660)) return false;
+            if (k >= Cfg::kItems && !mbar_wait(&bar[Cfg::B_IEMPTY + r], ph ^ 1u, abort_flag, tmo, 0x660)) return false;
             claimed[r] = static_cast<int>(i);
             mbar_arrive(&bar[Cfg::B_IFULL + r]);
             return true;
         }
-        if (!(role == kWarp ? wait_warp(&bar[Cfg::B_IFULL + r], ph, abort_flag, tmo, 0x661)
-                            : wait_one(&bar[Cfg::B_IFULL + r], ph, abort_flag, tmo, 0x662)))
+        if (!(role == kWarp ? mbar_wait_warp(&bar[Cfg::B_IFULL + r], ph, abort_flag, tmo, 0x661)
+                            : mbar_wait(&bar[Cfg::B_IFULL + r], ph, abort_flag, tmo, 0x662)))
             return false;
         i = claimed[r];
         if (role == kWarp) __syncwarp();
         if (lane == 0) mbar_arrive(&bar[Cfg::B_IEMPTY + r]);
         return true;
     };
-    // Calls f(unit, its state, reverse) for every item of this CTA until f gives up.
+    // Calls f(unit, its state, reverse, segment, chunks of the unit, first and last of the walk) for every item of this CTA
+    // until f gives up.
     auto items = [&](Role role, auto&& f) {
         for (int64_t k = 0;; ++k) {
             int64_t i;
@@ -320,19 +293,28 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 if (k * workers >= n_items) return true;
                 if (i >= n_items) continue;
             }
+            int seg = 0;
+            if (p.segs > 1) {
+                seg = static_cast<int>(i % p.segs);
+                i /= p.segs;
+            }
+            const bool rev = grad && (i & 1);
             int64_t u = grad ? i >> 1 : i;
             if (p.order != nullptr) u = static_cast<int64_t>(p.order[u / p.H]) * p.H + u % p.H;
-            if (!f(gated_unit(p, u), u, grad && (i & 1))) return false;
+            const GatedUnit un = gated_unit(p, u);
+            const int nch = (un.len + C - 1) / C, cc0 = seg * p.seg_chunks, cc1 = min(nch, cc0 + p.seg_chunks);
+            if (cc0 >= cc1 || (p.sums && cc1 == nch)) continue;  // (nothing starts from the last one's sum)
+            if (!f(un, u, rev, seg, nch, cc0, cc1)) return false;
         }
     };
-    // Calls f(unit, reverse, chunk, rows of it, chunks before it) for every chunk of them.
+    // Calls f(unit, reverse, chunk, rows of it, chunks before it, item, whether it begins the item) for every chunk of them.
     auto walk = [&](Role role, auto&& f) -> bool {
         int64_t g = 0;
-        return items(role, [&](const GatedUnit& un, int64_t, bool rev) {
-            const int nch = (un.len + C - 1) / C;
-            for (int cc = 0; cc < nch; ++cc, ++g) {
+        return items(role, [&](const GatedUnit& un, int64_t u, bool rev, int seg, int nch, int cc0, int cc1) {
+            const int64_t item = ((rev ? p.n_units : 0) + u) * p.segs + seg;
+            for (int cc = cc0; cc < cc1; ++cc, ++g) {
                 const int c = rev ? nch - 1 - cc : cc;
-                if (!f(un, rev, c, min(C, un.len - c * C), g)) return false;
+                if (!f(un, rev, c, min(C, un.len - c * C), g, item, cc == cc0)) return false;
             }
             return true;
         });
@@ -346,10 +328,10 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 group = static_cast<int>(un.row0 / p.rows);
                 row = static_cast<int>(r - group * p.rows);
             };
-            const bool ok = walk(kProducer, [&](const GatedUnit& un, bool rev, int c, int, int64_t g) {
+            const bool ok = walk(kProducer, [&](const GatedUnit& un, bool rev, int c, int, int64_t g, int64_t, bool) {
                 const int s = static_cast<int>(g % Cfg::NS);
                 if (g >= Cfg::NS &&
-                    !wait_one(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x600 + s))
+                    !mbar_wait(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x600 + s))
                     return false;
                 const CUtensorMap* mx = rev ? &m.q : &m.k;
                 const CUtensorMap* my = rev ? &m.d_o : &m.v;
@@ -382,11 +364,11 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         if (lane == 0) {
             constexpr uint32_t kId = idesc_bf16_f32(D, D, !Cfg::TS, true);
             bool issued = false;
-            walk(kLane, [&](const GatedUnit&, bool, int, int, int64_t g) {
+            walk(kLane, [&](const GatedUnit&, bool, int, int, int64_t g, int64_t, bool) {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g % Cfg::NU), l = static_cast<int>(g % Cfg::NL);
-                if (!wait_one(&bar[Cfg::B_SCALED + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x610 + s)) return false;
+                if (!mbar_wait(&bar[Cfg::B_SCALED + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x610 + s)) return false;
                 if (g >= Cfg::NU &&
-                    !wait_one(&bar[Cfg::B_UEMPTY + b], ((g / Cfg::NU) + 1) & 1, abort_flag, tmo, 0x618 + b))
+                    !mbar_wait(&bar[Cfg::B_UEMPTY + b], ((g / Cfg::NU) + 1) & 1, abort_flag, tmo, 0x618 + b))
                     return false;
                 tc_fence_after();
                 const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE,
@@ -419,7 +401,8 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         }
         __syncwarp();
     } else if (warp == 2) {
-        walk(kWarp, [&](const GatedUnit& un, bool rev, int c, int nv, int64_t g) {
+        float decay = 0.f;  // log2 of the segment's
+        walk(kWarp, [&](const GatedUnit& un, bool rev, int c, int nv, int64_t g, int64_t item, bool first) {
             const int s = static_cast<int>(g % Cfg::NS);
             float x[4], w[4], all;
             load_gates(p, un.row0 + static_cast<int64_t>(c) * C, nv, x);
@@ -429,7 +412,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
             } else {
                 scan_down(x, w, all);
             }
-            if (g >= 2 && !wait_warp(&bar[Cfg::B_SCALED + (g - 2) % Cfg::NS], ((g - 2) / Cfg::NS) & 1, abort_flag,
+            if (g >= 2 && !mbar_wait_warp(&bar[Cfg::B_SCALED + (g - 2) % Cfg::NS], ((g - 2) / Cfg::NS) & 1, abort_flag,
                                           tmo, 0x620 + s))
                 return false;
             uint2* o = reinterpret_cast<uint2*>(smem + Cfg::OFF_W + (g % Cfg::NW) * 3 * C * 2);
@@ -445,6 +428,10 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 w[3] -= bf16_hi(h.y);
             }
             if (lane == 0) gam[g % Cfg::kGam] = ex2(all);
+            if (p.sums) {
+                decay = first ? all : decay + all;
+                if (lane == 0) p.seg_decays[item] = ex2(decay);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
             return true;
@@ -452,7 +439,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
     } else if (warp == 3) {
         // publish a chunk's slot once every part of its state is in global memory
         if (lane == 0 && p.queue != nullptr) {
-            walk(kLane, [&](const GatedUnit& un, bool, int c, int, int64_t g) {
+            walk(kLane, [&](const GatedUnit& un, bool, int c, int, int64_t g, int64_t, bool) {
                 const unsigned int want = static_cast<unsigned int>(g + 1) * (4 * Cfg::NPAN);
                 if (!wait_until(tmo, abort_flag, 0x650, [&] {
                         unsigned int have;
@@ -470,11 +457,11 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {
-        walk(kWarp, [&](const GatedUnit&, bool, int, int nv, int64_t g) {
+        walk(kWarp, [&](const GatedUnit&, bool, int, int nv, int64_t g, int64_t, bool) {
             const int s = static_cast<int>(g % Cfg::NS);
             const uint32_t ph = (g / Cfg::NS) & 1;
-            if (!wait_warp(&bar[Cfg::B_GFULL + s], ph, abort_flag, tmo, 0x630 + s)) return false;
-            if (!wait_warp(&bar[Cfg::B_FULL + s], ph, abort_flag, tmo, 0x638 + s)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], ph, abort_flag, tmo, 0x630 + s)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_FULL + s], ph, abort_flag, tmo, 0x638 + s)) return false;
             const uint32_t x = sbase + s * Cfg::STAGE, y = x + Cfg::TILE;
             const uint32_t* w = reinterpret_cast<const uint32_t*>(smem + Cfg::OFF_W + (g % Cfg::NW) * 3 * C * 2);
             // w x = hi + mid + lo for two values at a time, in paired bf16 arithmetic.  A product of two 8-bit
@@ -498,7 +485,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 if (nv < C)
                     for (int row = nv + (warp - 4); row < C; row += 8)
                         if (lane < 16) st_shared_v4(y + (lane >> 3) * kPanel + row * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
-                if (!lofree && !wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
+                if (!lofree && !mbar_wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
                     return false;
                 tc_fence_after();
                 const uint32_t tp = tmem + Cfg::tm_part(g % Cfg::NL, 0) + half * 32 + (static_cast<uint32_t>(sub * 32) << 16);
@@ -543,7 +530,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 tc_fence_before();
             } else {
                 const uint32_t lo = sbase + Cfg::OFF_LO + (g % Cfg::NL) * 2 * Cfg::TILE;
-                if (!lofree && !wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
+                if (!lofree && !mbar_wait_warp(&bar[Cfg::B_LOEMPTY + g % Cfg::NL], loph, abort_flag, tmo, 0x648))
                     return false;
                 // warp w takes rows 16 (w - 4) ..; its lanes four rows of eight 16-byte pieces at a time
                 const int r0 = (warp - 4) * 16 + (lane >> 3);
@@ -586,11 +573,16 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         auto count_stored = [&] {
             asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(stored)) : "memory");
         };
-        items(kWarp, [&](const GatedUnit& un, int64_t u, bool rev) {
-            const int nch = (un.len + C - 1) / C;
-            if (nch == 0) return true;
+        items(kWarp, [&](const GatedUnit& un, int64_t u, bool rev, int seg, int nch, int cc0, int cc1) {
+            const int64_t item = ((rev ? p.n_units : 0) + u) * p.segs + seg;
             const float* in = rev ? p.dstate : (p.state ? p.state : p.s0);
             float* out = rev ? p.dstate : p.state;
+            if (p.segs > 1) {
+                // offset so that the indices of `at` below hold
+                float* start = p.seg_states + (item - u) * D * D;
+                in = p.sums ? nullptr : start;
+                out = p.sums ? start : (cc1 == nch ? out : nullptr);
+            }
             const int64_t at = u * D * D + static_cast<int64_t>(row < 0 ? 0 : row) * D + half * 64;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -601,32 +593,33 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 S[4 * j + 3] = f.w;
             }
             uint8_t* slots = static_cast<uint8_t*>(rev ? p.e_states : p.s_states) + un.slot0 * Cfg::SB;
-            for (int cc = 0; cc < nch; ++cc, ++g) {
+            for (int cc = cc0; cc < cc1; ++cc, ++g) {
                 const int c = rev ? nch - 1 - cc : cc;
                 const int b = static_cast<int>(g % Cfg::NU);
-                // the state before this chunk, as bf16, to its slot
-                if (lane == 0) bulk_wait_group_read<0>();
-                __syncwarp();
-                if (row >= 0) {
+                if (!p.sums) {  // the state before this chunk, as bf16, to its slot
+                    if (lane == 0) bulk_wait_group_read<0>();
+                    __syncwarp();
+                    if (row >= 0) {
 #pragma unroll
-                    for (int ch = 0; ch < 8; ++ch)
-                        st_shared_v4(smem_u32(panel) + sw128_off(row, ch), pack_bf16x2(S[8 * ch], S[8 * ch + 1]),
-                                     pack_bf16x2(S[8 * ch + 2], S[8 * ch + 3]),
-                                     pack_bf16x2(S[8 * ch + 4], S[8 * ch + 5]),
-                                     pack_bf16x2(S[8 * ch + 6], S[8 * ch + 7]));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    const int off = half * Cfg::SB_PANEL + sub * kRows * 128;
-                    bulk_store(slots + static_cast<int64_t>(c) * Cfg::SB + off, smem + Cfg::OFF_SB + off, kRows * 128);
-                    bulk_commit_group();
-                    if (g > 0) {  // the part of the chunk before is in global memory
-                        bulk_wait_group<1>();
-                        count_stored();
+                        for (int ch = 0; ch < 8; ++ch)
+                            st_shared_v4(smem_u32(panel) + sw128_off(row, ch), pack_bf16x2(S[8 * ch], S[8 * ch + 1]),
+                                         pack_bf16x2(S[8 * ch + 2], S[8 * ch + 3]),
+                                         pack_bf16x2(S[8 * ch + 4], S[8 * ch + 5]),
+                                         pack_bf16x2(S[8 * ch + 6], S[8 * ch + 7]));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int off = half * Cfg::SB_PANEL + sub * kRows * 128;
+                        bulk_store(slots + static_cast<int64_t>(c) * Cfg::SB + off, smem + Cfg::OFF_SB + off, kRows * 128);
+                        bulk_commit_group();
+                        if (g > 0) {  // the part of the chunk before is in global memory
+                            bulk_wait_group<1>();
+                            count_stored();
+                        }
                     }
                 }
-                if (!wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) return false;
+                if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) return false;
                 tc_fence_after();
                 const float gamma = gam[g % Cfg::kGam];
 #pragma unroll
@@ -740,8 +733,8 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
         for (int64_t g = 0;; ++g) {
             const int r = static_cast<int>(g % Cfg::kRing);
             const uint32_t ph = static_cast<uint32_t>(g / Cfg::kRing) & 1;
-            if (!(one ? wait_one(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x770)
-                      : wait_warp(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x771)))
+            if (!(one ? mbar_wait(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x770)
+                      : mbar_wait_warp(&bar[Cfg::B_UFULL + r], ph, abort_flag, tmo, 0x771)))
                 return false;
             const int row = ring[r].x, group = ring[r].y, nv = ring[r].z;
             if (!one) __syncwarp();
@@ -776,7 +769,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                     }
                     const int r = static_cast<int>(g % Cfg::kRing), s = static_cast<int>(g % Cfg::NS);
                     if (g >= Cfg::kRing &&
-                        !wait_one(&bar[Cfg::B_UEMPTY + r], ((g / Cfg::kRing) + 1) & 1, abort_flag, tmo, 0x773))
+                        !mbar_wait(&bar[Cfg::B_UEMPTY + r], ((g / Cfg::kRing) + 1) & 1, abort_flag, tmo, 0x773))
                         return false;
                     ring[r].x = ch.row;
                     ring[r].y = ch.group;
@@ -792,7 +785,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                             tma_prefetch_l2_3d(&m.k, pn * 64, ch.row, ch.group);
                             tma_prefetch_l2_3d(&m.v, pn * 64, ch.row, ch.group);
                         }
-                        if (!wait_one(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x700 + s))
+                        if (!mbar_wait(&bar[Cfg::B_EMPTY + s], ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x700 + s))
                             return false;
                     }
                     mbar_arrive_expect_tx(&bar[Cfg::B_FULL + s], 3 * Cfg::TILE);
@@ -805,7 +798,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                                     ch.group);
                     }
                     started = g + 1;
-                    if (g >= 1 && !wait_one(&bar[Cfg::B_SEMPTY], (g + 1) & 1, abort_flag, tmo, 0x708)) return false;
+                    if (g >= 1 && !mbar_wait(&bar[Cfg::B_SEMPTY], (g + 1) & 1, abort_flag, tmo, 0x708)) return false;
                     mbar_arrive_expect_tx(&bar[Cfg::B_SFULL], Cfg::SB);
                     bulk_load(smem + Cfg::OFF_SB, state, Cfg::SB, &bar[Cfg::B_SFULL]);
                     loaded = g + 1;
@@ -824,9 +817,9 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
             bool issued = false;
             auto scores = [&](int64_t g) -> bool {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
-                if (!wait_one(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x710 + s)) return false;
+                if (!mbar_wait(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x710 + s)) return false;
                 // the buffer's last P, of chunk g - 2, is used up
-                if (g >= 2 && !wait_one(&bar[Cfg::B_PEMPTY + b], ((g >> 1) + 1) & 1, abort_flag, tmo, 0x718)) return false;
+                if (g >= 2 && !mbar_wait(&bar[Cfg::B_PEMPTY + b], ((g >> 1) + 1) & 1, abort_flag, tmo, 0x718)) return false;
                 tc_fence_after();
                 const uint32_t q = sbase + s * Cfg::STAGE, k = q + Cfg::TILE;
 #pragma unroll
@@ -839,9 +832,9 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
             };
             auto output = [&](int64_t g) -> bool {
                 const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
-                if (g >= 1 && !wait_one(&bar[Cfg::B_OEMPTY], (g + 1) & 1, abort_flag, tmo, 0x720)) return false;
-                if (!wait_one(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x724)) return false;
-                if (!wait_one(&bar[Cfg::B_SFULL], g & 1, abort_flag, tmo, 0x728)) return false;
+                if (g >= 1 && !mbar_wait(&bar[Cfg::B_OEMPTY], (g + 1) & 1, abort_flag, tmo, 0x720)) return false;
+                if (!mbar_wait(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x724)) return false;
+                if (!mbar_wait(&bar[Cfg::B_SFULL], g & 1, abort_flag, tmo, 0x728)) return false;
                 tc_fence_after();
                 const uint32_t q = sbase + s * Cfg::STAGE, v = q + 2 * Cfg::TILE, sb = sbase + Cfg::OFF_SB;
 #pragma unroll
@@ -850,7 +843,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                                 sdesc_sw128(sb + ks * 2048, Cfg::SB_PANEL, 1024), kIdO, ks > 0);
                 mma_commit(&bar[Cfg::B_SEMPTY]);
                 issued = true;
-                if (!wait_one(&bar[Cfg::B_PFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x730 + b)) return false;
+                if (!mbar_wait(&bar[Cfg::B_PFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x730 + b)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks)
@@ -878,7 +871,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
             scan_up(x, G);
             const float R = __shfl_sync(0xffffffffu, G[3], lane | 7);  // prefix at the end of the 32-token block
             // tiles landed: the slot's last readers are done
-            if (!wait_warp(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x740 + s)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_FULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x740 + s)) return false;
             float4* o = reinterpret_cast<float4*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES);
             o[lane] = make_float4(G[0], G[1], G[2], G[3]);
             if (lane < 24) o[32 + lane] = make_float4(ex2(R - G[0]), ex2(R - G[1]), ex2(R - G[2]), ex2(R - G[3]));
@@ -894,8 +887,8 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
         const int sub = warp & 3, half = (warp - 4) >> 2, row = sub * 32 + lane;
         walk(false, [&](const GatedChunk&, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS), b = static_cast<int>(g & 1);
-            if (!wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x750 + s)) return false;
-            if (!wait_warp(&bar[Cfg::B_AFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x758 + b)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x750 + s)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_AFULL + b], (g >> 1) & 1, abort_flag, tmo, 0x758 + b)) return false;
             tc_fence_after();
             const float* G = reinterpret_cast<const float*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES);
             const float* F = G + C;
@@ -947,9 +940,9 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
         const uint32_t lane_off = (static_cast<uint32_t>(sub * 32) << 16) + half * 64;
         walk(false, [&](const GatedChunk& ch, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
-            if (!wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x760 + s)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_GFULL + s], (g / Cfg::NS) & 1, abort_flag, tmo, 0x760 + s)) return false;
             const float f = ex2(reinterpret_cast<const float*>(smem + Cfg::OFF_G + s * Cfg::G_BYTES)[row]);
-            if (!wait_warp(&bar[Cfg::B_OFULL], g & 1, abort_flag, tmo, 0x768)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_OFULL], g & 1, abort_flag, tmo, 0x768)) return false;
             tc_fence_after();
             const uint32_t panel = sbase + s * Cfg::STAGE + half * kPanel;  // Q, read by both of its products
             uint16_t* out = static_cast<uint16_t*>(p.o) + (ch.row0 + row) * D + half * 64;
@@ -1008,14 +1001,14 @@ __device__ __forceinline__ void give_tmem(uint32_t tmem) {
     if (threadIdx.x < 32) tmem_dealloc(tmem, 512);
 }
 
-// The states of the gradient, both directions.
+// The states of the gradient, both directions; the sums of segments.
 template <int D>
 __global__ void __launch_bounds__(640, 1)
-    gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items) {
+    gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items, bool grad) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = aligned_smem(smem_raw);
     const uint32_t tmem = take_tmem(smem);
-    gated_states_body<D>(m, p, n_items, true, smem, tmem, blockIdx.x, gridDim.x);
+    gated_states_body<D>(m, p, n_items, grad, smem, tmem, blockIdx.x, gridDim.x);
     give_tmem(tmem);
 }
 
@@ -1023,7 +1016,8 @@ __global__ void __launch_bounds__(640, 1)
 // others, and those when they are done, take the chunks in that order.  So K, V and the states come from L2 the second
 // time, and the serial phase of few long sequences overlaps the other.  A CTA waits only for units that CTAs already
 // running have claimed: one of the first takes chunks only when every unit is claimed, and the device starts the others
-// after them.  So it does not matter how many of the CTAs are on the device at once.
+// after them.  So it does not matter how many of the CTAs are on the device at once.  (Roles by order of arrival at a
+// counter instead of by index: 445 us, not 362, at B8 H16 T8192, since the first to arrive sit close together.)
 template <int D>
 __global__ void __launch_bounds__(640, 1)
     gated_prefill_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items, int n_state) {
@@ -1192,7 +1186,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                 for (int k = 0; k < 6; ++k) {
                     const int t = order[k];
-                    if (g >= Cfg::NS && !wait_one(empty(s, t), ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x800 + t))
+                    if (g >= Cfg::NS && !mbar_wait(empty(s, t), ((g / Cfg::NS) + 1) & 1, abort_flag, tmo, 0x800 + t))
                         return false;
                     if (t == Cfg::F_S || t == Cfg::F_E) {
                         mbar_arrive_expect_tx(full(s, t), Cfg::SB);
@@ -1240,7 +1234,7 @@ __global__ void __launch_bounds__(640, 1)
             constexpr uint32_t kIdW = idesc_bf16_f32(C, D, true, true);     // W K, W held transposed
             bool issued = false;
             auto wait = [&](int b, int64_t phase, unsigned where) {
-                return wait_one(&bar[b], static_cast<uint32_t>(phase & 1), abort_flag, tmo, where);
+                return mbar_wait(&bar[b], static_cast<uint32_t>(phase & 1), abort_flag, tmo, where);
             };
             walk([&](const GatedChunk& ch, int64_t, int64_t g) {
                 const int s = static_cast<int>(g % Cfg::NS);
@@ -1336,7 +1330,7 @@ __global__ void __launch_bounds__(640, 1)
             // (S: its tile was given back behind the last use of these decays' place.  V is waited for only where its
             // rows are zeroed: a full chunk's V may be given back, and loaded again, before this warp looks at it)
             for (int t : {Cfg::F_Q, Cfg::F_K, Cfg::F_O, Cfg::F_S, Cfg::F_V})
-                if ((t != Cfg::F_V || ch.nv < C) && !wait_warp(full(s, t), ph, abort_flag, tmo, 0x820 + t)) return false;
+                if ((t != Cfg::F_V || ch.nv < C) && !mbar_wait_warp(full(s, t), ph, abort_flag, tmo, 0x820 + t)) return false;
             float4* o = reinterpret_cast<float4*>(smem + Cfg::OFF_G + (g & 1) * 4 * C * 4);
             o[lane] = make_float4(G[0], G[1], G[2], G[3]);
             o[32 + lane] = make_float4(ex2(G[0]), ex2(G[1]), ex2(G[2]), ex2(G[3]));
@@ -1350,7 +1344,7 @@ __global__ void __launch_bounds__(640, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);
             // dv, the last result of the chunk
-            if (!wait_warp(&bar[Cfg::B_STAGED + 2], static_cast<uint32_t>(g & 1), abort_flag, tmo, 0x834)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_STAGED + 2], static_cast<uint32_t>(g & 1), abort_flag, tmo, 0x834)) return false;
             if (lane == 0) {
                 if (ch.nv == C) {
                     store_tile<D>(&m.dv, smem + s * Cfg::STAGE + Cfg::O, ch);
@@ -1367,7 +1361,7 @@ __global__ void __launch_bounds__(640, 1)
             const int s = static_cast<int>(g % Cfg::NS);
             const uint32_t gp = static_cast<uint32_t>(g & 1);
             auto store = [&](int n, int tile, const CUtensorMap* map) {
-                if (!wait_warp(&bar[Cfg::B_STAGED + n], gp, abort_flag, tmo, 0x832 + n)) return false;
+                if (!mbar_wait_warp(&bar[Cfg::B_STAGED + n], gp, abort_flag, tmo, 0x832 + n)) return false;
                 if (lane == 0 && ch.nv == C) store_tile<D>(map, smem + s * Cfg::STAGE + tile * Cfg::TILE, ch);
                 return true;
             };
@@ -1379,7 +1373,7 @@ __global__ void __launch_bounds__(640, 1)
                 mbar_arrive(empty(s, Cfg::F_K));
             }
             __syncwarp();
-            if (!wait_warp(&bar[Cfg::B_SUMS], gp, abort_flag, tmo, 0x830)) return false;
+            if (!mbar_wait_warp(&bar[Cfg::B_SUMS], gp, abort_flag, tmo, 0x830)) return false;
             const float* es = reinterpret_cast<const float*>(smem + Cfg::OFF_ES);
             auto get = [&](int off, float (&x)[4]) {
                 const float4* a = reinterpret_cast<const float4*>(smem + off);
@@ -1432,7 +1426,7 @@ __global__ void __launch_bounds__(640, 1)
             const uint32_t ph = (g / Cfg::NS) & 1, gp = static_cast<uint32_t>(g & 1);
             const uint32_t st = sbase + s * Cfg::STAGE;
             auto wait = [&](int b, uint32_t parity, unsigned where) {
-                return wait_warp(&bar[b], parity, abort_flag, tmo, where);
+                return mbar_wait_warp(&bar[b], parity, abort_flag, tmo, where);
             };
             auto arrive = [&](int b) {
                 __syncwarp();
@@ -1610,12 +1604,12 @@ cudaError_t raise_smem(PerDeviceOnce& once, F kern, int bytes) {
 unsigned grid_for(int64_t items, int num_sms) { return static_cast<unsigned>(items < num_sms ? items : num_sms); }
 
 template <int D>
-cudaError_t states_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
+cudaError_t states_d(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
     cudaError_t e = raise_smem(once, gated_states_tc_kernel<D>, StCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t items = 2 * p.n_units;
-    gated_states_tc_kernel<D><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items);
+    const int64_t items = p.n_units * p.segs * (grad ? 2 : 1);
+    gated_states_tc_kernel<D><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items, grad);
     return cudaGetLastError();
 }
 template <int D>
@@ -1628,11 +1622,11 @@ cudaError_t prefill_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cu
     // 90 and 100 %: B8 H16 T8192 466 369 369 369 382 382 us, B16 H32 T256 137 102 86 80 82 81, B4 H32 T512 59 46 46 46 43
     // 43, 24 packed sequences 288 233 239 225 231 209 (all d 128).
     const int most = std::max(1, num_sms * 75 / 100);
-    const int64_t rounds = (p.n_units + most - 1) / most;
-    const int n_state = static_cast<int>((p.n_units + rounds - 1) / rounds);
+    const int64_t items = p.n_units * p.segs, rounds = (items + most - 1) / most;
+    const int n_state = static_cast<int>((items + rounds - 1) / rounds);
     const int64_t slots = p.groups * p.nc;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(num_sms, n_state + slots)));
-    gated_prefill_tc_kernel<D><<<grid, OutCfg<D>::kThreads, kSmem, s>>>(m, p, p.n_units, n_state);
+    gated_prefill_tc_kernel<D><<<grid, OutCfg<D>::kThreads, kSmem, s>>>(m, p, items, n_state);
     return cudaGetLastError();
 }
 template <int D>
@@ -1647,8 +1641,8 @@ cudaError_t grad_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaS
 
 }  // namespace
 
-cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
-    return p.dk == 128 ? states_d<128>(p, m, num_sms, s) : states_d<64>(p, m, num_sms, s);
+cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s) {
+    return p.dk == 128 ? states_d<128>(p, m, grad, num_sms, s) : states_d<64>(p, m, grad, num_sms, s);
 }
 cudaError_t launch_gated_prefill_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
     return p.dk == 128 ? prefill_d<128>(p, m, num_sms, s) : prefill_d<64>(p, m, num_sms, s);

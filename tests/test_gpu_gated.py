@@ -155,6 +155,20 @@ def test_long_and_few_units(dtype, dk, dv):
     check_backward(x, dtype, s0=False)
 
 
+@pytest.mark.parametrize("kind", ["mild", "resets", "cliff", None])
+@pytest.mark.parametrize("dtype,dk,dv,T,lens", [(BF16, 128, 128, 2200, None), (BF16, 64, 64, 2048, None), (F32, 40, 64, 515, None),
+                                               (BF16, 24, 56, 300, None), (BF16, 128, 128, 2700, [0, 2500, 150]),
+                                               (BF16, 64, 64, 4500, [513, 0, 3900, 1]), (F32, 33, 20, 700, [10, 600, 0, 70])])
+def test_walk_in_segments(kind, dtype, dk, dv, T, lens):
+    """Few long units: their walk is cut into four or more segments.  Sequences shorter than one, ends inside one."""
+    x = make(41, dtype, 1, 2, T, dk, dv, kind, lens)
+    if lens is not None:
+        for m in ("q", "k", "v", "do"):
+            x[m][:, :, sum(lens):] = float("nan")
+    check_prefill(x, dtype)
+    check_backward(x, dtype)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("B,H,T,lens", [(2, 16, 4096, None), (1, 24, 6000, None), (1, 16, 5555, [3000, 1, 0, 700, 129, 1725])])
 def test_many_chunks(d, B, H, T, lens):
