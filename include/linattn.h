@@ -167,9 +167,9 @@ la_status la_decode_step(const void* q, const void* k, const void* v, void* o,
  * ------------------------------------------------------------------------- */
 
 /* Prefill of the gated recurrence, dense or packed; the parameters of
- * la_prefill, with g.  Two phases: the states at the chunk edges go to the
- * workspace, then every chunk is computed on its own, so few long sequences
- * use the whole device too.
+ * la_prefill, with g.  The states at the chunk edges go to the workspace, and
+ * every chunk is computed on its own from there; few long sequences are walked
+ * in segments.
  *   workspace: la_gated_prefill_workspace_size() bytes, 16-byte aligned, free
  *     for the library until the call's work on `stream` has finished; calls
  *     that may overlap (and captured graphs that may run at once) need one
@@ -177,13 +177,16 @@ la_status la_decode_step(const void* q, const void* k, const void* v, void* o,
  *   max_seqlen: packed mode only, an upper bound on every sequence length
  *     (0 = unknown); at most 16 runs the few-token kernel, with the
  *     consequences that la_prefill describes, and needs no workspace.
- * Kernels: at most 16 tokens per unit and d_v a multiple of 4 that splits a
- * block (la_gated_prefill_kernel says "short"): one pass over the state.
- * Otherwise fp32 CUDA cores in chunks of 32 tokens.  Errors:
+ * Kernels (la_gated_prefill_kernel): "short", at most 16 tokens per unit and
+ * d_v a multiple of 4 that splits a block: one pass over the state.  "tc",
+ * bf16 with d_k == d_v in {64, 128}: tensor cores, chunks of 128 tokens.
+ * "simt", all else: fp32 CUDA cores, chunks of 32 tokens.  Errors:
  * LA_ERR_INVALID_ARG (as for la_prefill; a workspace that is missing, too
  * small or misaligned: la_last_cuda_error() then says what was needed),
- * LA_ERR_UNSUPPORTED (d_k or d_v above 128; T above 2^31 - 1; a state that is
- * not 16-byte aligned on the few-token path). */
+ * LA_ERR_UNSUPPORTED (d_k or d_v above 128; T above 2^31 - 1; more than
+ * 2^31 - 1 chunks or 2^28 units; "tc": a tensor other than g that is not
+ * 16-byte aligned; "short": such a state).  A bounded wait that expired inside
+ * the kernel shows in la_device_status(), as for la_prefill. */
 la_status la_gated_prefill(const void* q, const void* k, const void* v,
                            const void* g, void* o, float* state,
                            la_dtype dtype, int B, int H, int64_t T, int d_k,
@@ -196,8 +199,8 @@ size_t la_gated_prefill_workspace_size(la_dtype dtype, int B, int H, int64_t T,
                                        int d_k, int d_v, int num_seqs);
 
 /* Which kernel la_gated_prefill runs: max_tokens is T for dense input and
- * max_seqlen for packed input.  "short", "simt" or "unsupported".  Host
- * only. */
+ * max_seqlen for packed input.  "short", "tc", "simt" or "unsupported".  Host
+ * only.  The gradient has no "short" kernel. */
 const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens,
                                     int d_k, int d_v);
 

@@ -19,9 +19,10 @@
 // a sum over exactly the (source, reader) pairs whose path crosses gate t: no
 // two large terms are subtracted over a long range.
 //
-// Both directions run in two phases.  The state phase walks the chunks of a
-// unit in order (in reverse for E) and writes the state at every chunk's edge
-// to the workspace; the chunk phase then computes all chunks independently.
+// The state phase walks the chunks of a unit in order (in reverse for E) and
+// writes the state at every chunk's edge to the workspace; the chunk phase
+// computes all chunks independently (in the tensor-core prefill the same launch,
+// each chunk as soon as its state is there; else the next one).
 #pragma once
 
 #include <cuda.h>

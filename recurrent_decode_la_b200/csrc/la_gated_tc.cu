@@ -2,24 +2,31 @@
 // (bf16, d_k == d_v == D in {64, 128}, chunks of 128 tokens).  The formulas
 // stand in la_gated.h.
 //
-// Three kernels.  gated_states_tc walks the chunks of a unit and writes the
-// state at every chunk's start (and, for the gradient, in reverse the gradient
-// of the state at every chunk's end); it is the only serial part, and its
-// per-chunk product needs no earlier state, so the chain is one multiply-add
-// per element and chunk.  gated_out_tc and gated_grad_tc then take all chunks
-// in any order, one at a time per SM.
+// Three kernels.  gated_prefill_tc does the prefill in one launch: some of its
+// CTAs walk the chunks of the units and write the state at every chunk's start,
+// the only serial part; the others turn chunks whose state is there into
+// outputs.  For the gradient gated_states_tc walks the units in both directions
+// and gated_grad_tc then takes the chunks in any order.  A chunk's addition to
+// the state needs no earlier state, so the chain is one multiply-add per element
+// and chunk.
 //
-// All three are bound by memory traffic.  Per 128 tokens at D = 128 the states
-// cost 96 KB (K and V read, a bf16 state written), the output 160 KB, the
-// gradient 288 KB, against the least possible 128 KB forward and 224 KB
-// backward.
+// HBM does not bind them.  Per 128 tokens at D = 128 the prefill moves 1.08 times
+// the 128 KB that it must (the second reading of K and V and that of the states
+// hit L2), at 25 to 35 % of the copy rate; what binds it is the time of an SM:
+// 2.3 us of a CTA for the state of a chunk (three products of 128^3 on decayed
+// keys, whose splitting takes as long as the products), 3.7 us for its output.
+// B8 H16 T8192: 372 us on a cool device and 415 in a long run, where the floor of
+// its bytes is 167.  The gradient makes both states (145 us at B4 H16 T8192) and
+// then computes a chunk in about 16k clocks, a chain of seven products and the
+// steps between them, of which the tensor cores work 20 %: 272 us; in all 440 to
+// 480 us, floor 145.
 //
 // Rounding.  Sums, states and decays are fp32.  An operand of a product is
 // rounded to bf16 once where its result is bf16 too (decayed scores, chunk
 // states).  Where the result is an fp32 state, the decayed keys (queries) are
 // kept as the sum of three bf16 numbers, 2^-24 of them, at the price of two
-// more products (two parts would leave the state 2.5e-6 of itself off).  A row's decay is applied to the fp32 accumulator, not to a bf16
-// operand.  The tensor core drops bits when it adds to an accumulator: a state
+// more products (two parts would leave the state 2.4e-6 of itself off, three
+// 1e-7).  A row's decay is applied to the fp32 accumulator, not to a bf16 operand.  The tensor core drops bits when it adds to an accumulator: a state
 // summed there over 8192 tokens is off by 9e-6 of itself, so the states live in
 // registers and an accumulator spans one chunk only.
 //

@@ -233,6 +233,20 @@ def test_decode(dtype, dk, dv, B, H, kind):
     assert ref.rel(torch.stack(outs, 2), oo) <= TOL[dtype] and ref.rel(S, SS) <= TOL_STATE
 
 
+@pytest.mark.parametrize("dtype,dk,dv", [(F32, 128, 96), (BF16, 90, 100), (F32, 33, 50), (F32, 128, 127), (BF16, 3, 2), (F32, 1, 1)])
+@pytest.mark.parametrize("units", [1, 148, 149, 296, 297, 700])
+@pytest.mark.parametrize("off", [0, 1, 2])
+def test_decode_sizes(dtype, dk, dv, units, off):
+    """Head sizes of every divisibility, unit counts around the changes of kernel, states off 16-byte boundaries."""
+    x = make(units, dtype, units, 1, 1, dk, dv)
+    S = torch.empty(units * dk * dv + off, device=DEV)[off:].view(units, dk, dv)
+    S.copy_(x["S0"])
+    o = torch.full((units, 1, dv), float("nan"), dtype=dtype, device=DEV)
+    la.la_gated_decode_step(*(x[m][:, :, 0].contiguous() for m in "qkvg"), o, S)
+    oo, SS = ref.prefill(x["q"], x["k"], x["v"], x["g"], x["S0"])
+    assert ref.rel(o[:, :, None], oo) <= TOL[dtype] and ref.rel(S, SS) <= TOL_STATE
+
+
 @pytest.mark.parametrize("dtype,dk,dv", [(BF16, 128, 128), (F32, 48, 80), (BF16, 64, 64)])
 def test_together(dtype, dk, dv):
     """As a model uses them: positions on q and k, the prompt, drafted tokens, single tokens; one long call agrees."""
