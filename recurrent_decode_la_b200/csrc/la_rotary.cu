@@ -22,7 +22,9 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 2;  // heads in flight per thread and tensor (4 and 8 with fewer CTAs: up to 8 % slower)
+// Heads in flight per thread and tensor.  16-byte vectors: two (4 and 8 with fewer CTAs: up to 8 % slower); narrower ones, of
+// which a thread moves less at a time, four (eight spilled registers).
+constexpr int batch_of(int bytes) { return bytes >= 16 ? 2 : 4; }
 // Above this (bytes read and written) nothing of the tensors is left in L2 for the next kernel anyway: loads and stores
 // then go past it (evict first).  B8 H16 T8192 d128: 169 us, as a plain copy, against 212 us with the default policy.
 constexpr int64_t kStreamBytes = 126 << 20;
@@ -31,10 +33,21 @@ template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
     T x[V];
 };
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> { using type = int4; };
+template <>
+struct Word<8> { using type = int2; };
+template <>
+struct Word<4> { using type = int; };
+template <>
+struct Word<2> { using type = short; };
 template <bool STREAM, typename W>
 __device__ __forceinline__ W load_vec(const W* p) {
+    using I = typename Word<sizeof(W)>::type;
     if constexpr (STREAM) {
-        const int4 r = __ldcs(reinterpret_cast<const int4*>(p));
+        const I r = __ldcs(reinterpret_cast<const I*>(p));
         return *reinterpret_cast<const W*>(&r);
     } else {
         return *p;
@@ -42,8 +55,9 @@ __device__ __forceinline__ W load_vec(const W* p) {
 }
 template <bool STREAM, typename W>
 __device__ __forceinline__ void store_vec(W* p, const W& x) {
+    using I = typename Word<sizeof(W)>::type;
     if constexpr (STREAM)
-        __stcs(reinterpret_cast<int4*>(p), *reinterpret_cast<const int4*>(&x));
+        __stcs(reinterpret_cast<I*>(p), *reinterpret_cast<const I*>(&x));
     else
         *p = x;
 }
@@ -67,6 +81,7 @@ __device__ __forceinline__ int packed_place(const int32_t* cu, int num_seqs, int
 // One thread: V pairs (or V passed elements) of one token, heads h0 .. h0 + heads - 1 of both tensors.
 template <typename T, int V, bool INTERLEAVED, bool STREAM>
 __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryProblem p, int items, int heads) {
+    constexpr int kBatch = batch_of(sizeof(T) * V);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     if (i >= p.B * p.T * items) return;
@@ -90,8 +105,15 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryProblem
             const T* x = static_cast<const T*>(p.x[which]);
             T* y = static_cast<T*>(p.y[which]);
             if (x == nullptr || x == y) continue;
-            for (int64_t h = 0; h < h1 - h0; ++h)
-                *reinterpret_cast<Vec<T, V>*>(y + at + h * step) = *reinterpret_cast<const Vec<T, V>*>(x + at + h * step);
+            for (int64_t hb = 0; hb < h1 - h0; hb += kBatch) {
+                Vec<T, V> u[kBatch];
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n)
+                    if (hb + n < h1 - h0) u[n] = load_vec<STREAM>(reinterpret_cast<const Vec<T, V>*>(x + at + (hb + n) * step));
+#pragma unroll
+                for (int n = 0; n < kBatch; ++n)
+                    if (hb + n < h1 - h0) store_vec<STREAM>(reinterpret_cast<Vec<T, V>*>(y + at + (hb + n) * step), u[n]);
+            }
         }
         return;
     }
@@ -152,10 +174,9 @@ cudaError_t rotary_v(const RotaryProblem& p, int num_sms, cudaStream_t s) {
     const int heads = static_cast<int>((p.H + groups - 1) / groups);
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((p.H + heads - 1) / heads));
     const int64_t bytes = 2 * p.B * p.H * p.T * p.d * static_cast<int64_t>(sizeof(T)) * (p.x[1] ? 2 : 1);
-    constexpr bool kWide = sizeof(T) * V == 16;
-    const bool stream = kWide && bytes > kStreamBytes;
-    const auto kern = p.interleaved ? (stream ? rotary_kernel<T, V, true, kWide> : rotary_kernel<T, V, true, false>)
-                                    : (stream ? rotary_kernel<T, V, false, kWide> : rotary_kernel<T, V, false, false>);
+    const bool stream = bytes > kStreamBytes;
+    const auto kern = p.interleaved ? (stream ? rotary_kernel<T, V, true, true> : rotary_kernel<T, V, true, false>)
+                                    : (stream ? rotary_kernel<T, V, false, true> : rotary_kernel<T, V, false, false>);
     return launch_pdl(kern, grid, dim3(kThreads), 0, s, p, items, heads);
 }
 
@@ -179,13 +200,18 @@ __global__ void rotary_init_kernel(float* freq, int rot, double base, int scalin
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryProblem& p, int num_sms, cudaStream_t s) {
-    const int size = p.dtype ? 2 : 4, v = 16 / size;
     uintptr_t bits = 0;
     for (int w = 0; w < 2; ++w) bits |= reinterpret_cast<uintptr_t>(p.x[w]) | reinterpret_cast<uintptr_t>(p.y[w]);
-    // 16-byte accesses where every vector of a row is aligned and whole
-    const bool vec = bits % 16 == 0 && p.d % v == 0 && (p.rot / 2) % v == 0;
-    if (p.dtype) return vec ? rotary_v<__nv_bfloat16, 8>(p, num_sms, s) : rotary_v<__nv_bfloat16, 1>(p, num_sms, s);
-    return vec ? rotary_v<float, 4>(p, num_sms, s) : rotary_v<float, 1>(p, num_sms, s);
+    // the widest accesses at which every vector of a row is aligned and whole (8 x 16 heads of 4096, bf16, interleaved, 36 of
+    // 128 turned: 221 us with two elements, 672 with one)
+    auto fits = [&](int v) { return bits % (v * (p.dtype ? 2 : 4)) == 0 && p.d % v == 0 && (p.rot / 2) % v == 0; };
+    if (p.dtype) {
+        using T = __nv_bfloat16;
+        return fits(8) ? rotary_v<T, 8>(p, num_sms, s) : fits(4) ? rotary_v<T, 4>(p, num_sms, s)
+             : fits(2) ? rotary_v<T, 2>(p, num_sms, s) : rotary_v<T, 1>(p, num_sms, s);
+    }
+    return fits(4) ? rotary_v<float, 4>(p, num_sms, s) : fits(2) ? rotary_v<float, 2>(p, num_sms, s)
+                                                                 : rotary_v<float, 1>(p, num_sms, s);
 }
 
 cudaError_t launch_rotary_init(float* freq, int rot, double base, int scaling, double factor, double original,

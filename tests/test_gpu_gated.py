@@ -395,6 +395,32 @@ def test_rotary(dtype, d, rot, interleaved):
     assert ref.rel(one, ref.f64(q)) <= (2 * 2.0 ** -8 if dtype == BF16 else 2.0 ** -19)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d,rot", [(96, 88), (64, 36), (72, 20), (128, 50)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,H,T", [(1, 9, 5), (2, 16, 700), (8, 16, 2000)])
+def test_rotary_widths(dtype, d, rot, interleaved, B, H, T):
+    """Accesses of every width, few heads a thread and many, and tensors above the size from which they stream."""
+    gen = torch.Generator(device=DEV).manual_seed(d + T)
+    q, k = (torch.randn(B, H, T, d, generator=gen, device=DEV).to(dtype) for _ in range(2))
+    freq = torch.empty(rot // 2, device=DEV)
+    la.la_rotary_init(freq)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    la.la_rotary(q, k, qo, ko, freq, interleaved=interleaved)
+    angle = torch.arange(T, device=DEV).double()[:, None] * freq.double()
+    c, s = angle.cos(), angle.sin()
+    for x, y in ((q, qo), (k, ko)):
+        x, y = x.double(), y.double()
+        a, b = (x[..., 0:rot:2], x[..., 1:rot:2]) if interleaved else (x[..., :rot // 2], x[..., rot // 2:rot])
+        want = x.clone()
+        if interleaved:
+            want[..., 0:rot:2], want[..., 1:rot:2] = a * c - b * s, b * c + a * s
+        else:
+            want[..., :rot // 2], want[..., rot // 2:rot] = a * c - b * s, b * c + a * s
+        assert float((y - want).norm() / want.norm()) <= (2.0 ** -8 if dtype == BF16 else 2.0 ** -20)
+        assert torch.equal(y[..., rot:], want[..., rot:])
+
+
 @pytest.mark.parametrize("lens,behind", [([5, 0, 20, 1], 3), ([40], 0), ([0, 3], 0)])
 def test_rotary_packed(lens, behind):
     gen = torch.Generator().manual_seed(1)
