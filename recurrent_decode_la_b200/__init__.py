@@ -3,7 +3,9 @@
 Chunkwise-parallel prefill and one-token decode, as in the slides
 "Chunking, causality, and parallel prefill": per chunk of C tokens
 O = tril(Q K^T) V + Q S_in and S_out = S_in + K^T V; decode is the same
-mechanism for one token, S <- S + k v^T, o = q^T S.
+mechanism for one token, S <- S + k v^T, o = q^T S.  Beside it the gated
+recurrence S <- e^g S + k v^T (prefill, its gradient, one token) and the
+rotary positions of q and k.
 
 Every step runs in the CUDA library ``liblinattn.so`` (C ABI declared in
 ``include/linattn.h``).  This package is a thin ctypes binding with the same

@@ -10,16 +10,18 @@
 // the state needs no earlier state, so the chain is one multiply-add per element
 // and chunk.
 //
-// HBM does not bind them.  Per 128 tokens at D = 128 the prefill moves 1.08 times
-// the 128 KB that it must (the second reading of K and V and that of the states
-// hit L2), at 25 to 35 % of the copy rate; what binds it is the time of an SM:
-// 2.3 us of a CTA for the state of a chunk (three products of 128^3 on decayed
-// keys, whose splitting takes as long as the products), 3.7 us for its output.
-// B8 H16 T8192: 372 us on a cool device and 415 in a long run, where the floor of
-// its bytes is 167.  The gradient makes both states (145 us at B4 H16 T8192) and
-// then computes a chunk in about 16k clocks, a chain of seven products and the
-// steps between them, of which the tensor cores work 20 %: 272 us; in all 440 to
-// 480 us, floor 145.
+// What binds them is first the time of an SM, then memory.  A chunk's state costs
+// a CTA 2.3 us (three products of 128^3 on decayed keys, whose splitting takes as
+// long as the products), its output 3.7 us.  Per 128 tokens at D = 128 the prefill
+// has to move 128 KB.  It moves 1.08 times that while the second reading of K and
+// V and that of the states hit L2 (B2 H16 T4096), twice that when the states run
+// further ahead than L2 reaches (B8 H16 T4096: 1032 MB in 196 us, 80 % of the copy
+// rate; evict-first policies on the second readings changed nothing).  B8 H16
+// T8192: 372 us on a cool device and 415 in a long run; the floor of its bytes is
+// 167.  The gradient moves 955 MB at B4 H16 T4096 where 483 are the least: both
+// states at 72 % of the copy rate (145 us of B4 H16 T8192), then the chunks at
+// 58 %, each a chain of seven products and the steps between them that takes a CTA
+// 16k clocks (272 us); in all 440 to 480 us, floor 145.
 //
 // Rounding.  Sums, states and decays are fp32.  An operand of a product is
 // rounded to bf16 once where its result is bf16 too (decayed scores, chunk
