@@ -36,12 +36,14 @@ constexpr int64_t kPlanSms = 148;
 
 // Chunk states in the workspace: packed, first the chunk offsets (num_seqs + 1
 // int32) and the sequences by length (num_seqs int32); for the tensor-core prefill
-// the queue of published chunks; then one state per chunk slot, and for the gradient one gradient of
-// a state per slot.
+// the queue of published chunks; room for the sums of segments and their decays;
+// then one state per chunk slot, and for the gradient one gradient of a state per
+// slot.
 struct Layout {
     int chunk = 0;
     int64_t nc = 0;
     int segs = 1, seg_chunks = 0;
+    int64_t seg_slots = 0;
     size_t queue = 0, seg = 0, s = 0, e = 0, bytes = 0;
 };
 Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs, bool grad) {
@@ -57,17 +59,17 @@ Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs
     // the second walk costs what it saves (two tensor-core chunks, 2 heads of 1000 tokens: 43 us, unsplit 35).  Unsplit
     // and split: 8 heads of 16384 tokens 270 and 114 us, their gradient 310 and 183; 8 heads of 4000 83 and 59; fp32, 4
     // heads of 8000 180 and 75, their gradient 751 and 242.
-    const int64_t units = groups * std::max(1, num_seqs), nch = (T + w.chunk - 1) / w.chunk;
-    const int64_t ctas = units * (grad ? 2 : 1) * (kind == kTc ? 1 : (dv + 31) / 32);
-    const int64_t room = kind == kSimt ? 2 * kPlanSms : grad ? kPlanSms : kPlanSms * 3 / 4;
-    int64_t segs = std::min<int64_t>({room / ctas, nch / (kind == kTc ? 4 : 2), 64});
-    if (segs < 4) segs = 1;
+    const int64_t units = groups * std::max(1, num_seqs), nch = (T + w.chunk - 1) / w.chunk, dirs = grad ? 2 : 1;
+    const int64_t room = (kind == kSimt ? 2 * kPlanSms / ((dv + 31) / 32) : grad ? kPlanSms : kPlanSms * 3 / 4) / dirs;
+    const int64_t most = std::min<int64_t>(nch / (kind == kTc ? 4 : 2), 64);
+    const int64_t segs = std::min(room / units, most) < 4 ? 1 : std::min(room / units, most);
     w.seg_chunks = static_cast<int>((nch + segs - 1) / segs);
     w.segs = static_cast<int>((nch + w.seg_chunks - 1) / w.seg_chunks);
+    // Room for the segments of any call with fewer units or tokens, so that a workspace fits those too.
+    w.seg_slots = most < 4 ? 0 : dirs * std::min(room, units * most);
     w.queue = num_seqs > 0 ? up256((2 * static_cast<size_t>(num_seqs) + 1) * 4) : 0;
     w.seg = w.queue + (kind == kTc && !grad ? up256((static_cast<size_t>(groups) * w.nc + kQueueHead) * 4) : 0);
-    w.s = w.seg;
-    if (w.segs > 1) w.s += up256(static_cast<size_t>(units) * (grad ? 2 : 1) * w.segs * (static_cast<size_t>(dk) * dv + 1) * 4);
+    w.s = w.seg + up256(static_cast<size_t>(w.seg_slots) * (static_cast<size_t>(dk) * dv + 1) * 4);
     w.e = w.s + states;
     w.bytes = w.e + (grad ? states : 0);
     return w;
@@ -105,7 +107,7 @@ la_status sizes(GatedProblem& p, la_dtype dtype, int B, int H, int64_t T, int dk
     return LA_OK;
 }
 
-la_status place(GatedProblem& p, const Layout& w, bool grad, void* workspace, size_t bytes) {
+la_status place(GatedProblem& p, const Layout& w, void* workspace, size_t bytes) {
     if (p.groups * w.nc > 0x7fffffffLL || p.n_units > (1 << 28)) return refuse(LA_ERR_UNSUPPORTED, "too many chunks for one call");
     if (!workspace || bytes < w.bytes || !aligned16(workspace)) {
         char why[128];
@@ -121,7 +123,7 @@ la_status place(GatedProblem& p, const Layout& w, bool grad, void* workspace, si
     p.order = p.cu && p.num_seqs <= kMaxGatedOrder ? p.choff + p.num_seqs + 1 : nullptr;
     if (w.segs > 1) {
         p.seg_states = reinterpret_cast<float*>(base + w.seg);
-        p.seg_decays = p.seg_states + static_cast<size_t>(p.n_units) * (grad ? 2 : 1) * w.segs * p.dk * p.dv;
+        p.seg_decays = p.seg_states + w.seg_slots * p.dk * p.dv;
     }
     p.s_states = base + w.s;
     p.e_states = base + w.e;
@@ -213,7 +215,7 @@ la_status la_gated_prefill(const void* q, const void* k, const void* v, const vo
         return e == cudaSuccess ? LA_OK : fail(e);
     }
     const Layout w = plan(kind, p.groups, T, d_k, d_v, p.num_seqs, false);
-    if ((st = place(p, w, false, workspace, workspace_bytes)) != LA_OK) return st;
+    if ((st = place(p, w, workspace, workspace_bytes)) != LA_OK) return st;
     p.q = q; p.k = k; p.v = v; p.g = g; p.o = o; p.state = state;
     if (kind == kTc) {
         GatedMaps m = {};
@@ -247,7 +249,7 @@ la_status la_gated_prefill_backward(const void* q, const void* k, const void* v,
         return refuse(LA_ERR_INVALID_ARG, "a tensor is NULL");
     const Kernel kind = choose(dtype, 0, d_k, d_v, true);
     const Layout w = plan(kind, p.groups, T, d_k, d_v, p.num_seqs, true);
-    if ((st = place(p, w, true, workspace, workspace_bytes)) != LA_OK) return st;
+    if ((st = place(p, w, workspace, workspace_bytes)) != LA_OK) return st;
     p.q = q; p.k = k; p.v = v; p.g = g;
     p.s0 = state0;
     p.d_o = d_o;

@@ -62,6 +62,21 @@ def test_kernel_choice(lib):
     assert la.la_gated_prefill_kernel(torch.bfloat16, 8, 129, 128) == "unsupported"
 
 
+@pytest.mark.parametrize("dtype,dk,dv", [(torch.bfloat16, 128, 128), (torch.bfloat16, 64, 64), (torch.float32, 128, 40)])
+@pytest.mark.parametrize("size", [la.la_gated_prefill_workspace_size, la.la_gated_prefill_backward_workspace_size])
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_workspace_fits_smaller_calls(lib, dtype, dk, dv, size, packed):
+    """A program sizes its workspace for the largest call: none with fewer sequences, heads or tokens needs more."""
+    Ts = [17, 128, 500, 1024, 2048, 2049, 5000, 5121, 8192, 40000]
+    for n in (1, 2, 5, 8, 27, 28, 60):
+        for H in (1, 3, 16):
+            sizes = [size(dtype, 1, H, T, dk, dv, n) if packed else size(dtype, n, H, T, dk, dv) for T in Ts]
+            assert sizes == sorted(sizes)
+    for T in Ts:
+        sizes = [size(dtype, 1, 1, T, dk, dv, n) if packed else size(dtype, n, 1, T, dk, dv) for n in range(1, 160)]
+        assert sizes == sorted(sizes)
+
+
 def test_workspace_sizes(lib):
     # a float32 state per chunk of 32 tokens and head; twice that for the gradient
     assert la.la_gated_prefill_workspace_size(torch.float32, 2, 3, 65, 64, 32) == 2 * 3 * 3 * 64 * 32 * 4
