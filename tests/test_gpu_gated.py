@@ -343,6 +343,53 @@ def test_two_calls_at_once():
         assert all(torch.equal(s, t) for s, t in zip(a, b))
 
 
+def test_prefills_at_once():
+    """Three streams whose launches share the device: each one's CTAs that wait and those that they wait for start when
+    others leave room.  Few units in segments, many units, packed ones."""
+    xs = [make(33, BF16, 1, 3, 6000, 128, 128), make(34, BF16, 12, 16, 900, 128, 128), make(35, BF16, 1, 16, 5000, 64, 64, "mild", [4000, 0, 1000])]
+    want = [[t.clone() for t in run_prefill(x)] for x in xs]
+    ws = [ws_for(x, False) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        got = [(torch.empty_like(x["v"]), x["S0"].clone()) for x in xs]
+        torch.cuda.synchronize()
+        for x, w, s, (o, S) in zip(xs, ws, streams, got):
+            with torch.cuda.stream(s):
+                la.la_gated_prefill(x["q"], x["k"], x["v"], x["g"], o, S, cu_seqlens=x["cu"], workspace=w)
+        torch.cuda.synchronize()
+        assert la.la_device_status() == la.LA_OK
+        for a, b in zip(got, want):
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+def test_one_workspace_for_calls_of_many_sizes():
+    """Sized for the largest call and used for each in turn, in order on one stream."""
+    ws = {b: ws_for(make(1, BF16, 28, 2, 2048, 128, 128), b) for b in (False, True)}
+    for B, T in ((28, 2048), (27, 2048), (1, 2048), (3, 1999), (1, 17), (28, 500)):
+        x = make(B + T, BF16, B, 2, T, 128, 128)
+        for fn, b in ((run_prefill, False), (run_backward, True)):
+            assert all(torch.equal(s, t) for s, t in zip(fn(x, ws=ws[b]), fn(x)))
+
+
+def test_more_than_2_31_elements():
+    """The last head of tensors of 2^31 elements and more, against a call of its own."""
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("needs 60 GB")
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    B, H, T, d = 1, 130, 131072, 128
+    q, k, v, do = (torch.randn(B, H, T, d, generator=gen, device=DEV, dtype=BF16).mul_(0.1) for _ in range(4))
+    g = -0.1 * torch.rand(B, H, T, generator=gen, device=DEV).to(BF16)
+    assert q.numel() > 1 << 31
+    x = dict(q=q, k=k, v=v, g=g, do=do, S0=torch.zeros(H, d, d, device=DEV), dS=torch.zeros(H, d, d, device=DEV), cu=None, lens=None)
+    y = {m: (t[:, -1:].contiguous() if t.dim() > 3 or m == "g" else t[-1:].clone()) for m, t in x.items() if t is not None}
+    y.update(cu=None, lens=None)
+    for fn, tail in ((run_prefill, lambda t: t[:, -1:]), (run_backward, lambda t: t[:, -1:])):
+        whole = [(t[-1:] if t.shape[0] == H else tail(t)).clone() for t in fn(x)]
+        torch.cuda.empty_cache()
+        for a, b in zip(whole, fn(y)):        # walked whole and in segments: two sums of the same products
+            assert float((a.double() - b.double()).norm() / b.double().norm()) <= (2 * TOL_STATE if a.dtype == F32 else 2.0 ** -8)
+
+
 def test_without_dg_and_bad_offsets():
     x = make(17, BF16, 1, 2, 300, 64, 64, None)
     out = [torch.empty_like(x[m]) for m in ("q", "k", "v")]
