@@ -57,8 +57,9 @@ Layout plan(Kernel kind, int64_t groups, int64_t T, int dk, int dv, int num_seqs
     // device works on it, where that leaves at most half of it one behind the other (with three segments 32 heads of
     // 4096 tokens took 118 us, unsplit 107).  From four tensor-core chunks a segment, or two of the CUDA cores: below,
     // the second walk costs what it saves (two tensor-core chunks, 2 heads of 1000 tokens: 43 us, unsplit 35).  Unsplit
-    // and split: 8 heads of 16384 tokens 270 and 114 us, their gradient 310 and 183; 8 heads of 4000 83 and 59; fp32, 4
-    // heads of 8000 180 and 75, their gradient 751 and 242.
+    // and split: 8 heads of 16384 tokens 270 and 101 us, their gradient 310 and 173; 8 heads of 4000 83 and 54; fp32, 4
+    // heads of 8000 180 and 70, their gradient 751 and 237 (with four CTAs of the CUDA cores an SM instead of two 78 and
+    // 244).
     const int64_t units = groups * std::max(1, num_seqs), nch = (T + w.chunk - 1) / w.chunk, dirs = grad ? 2 : 1;
     const int64_t room = (kind == kSimt ? 2 * kPlanSms / ((dv + 31) / 32) : grad ? kPlanSms : kPlanSms * 3 / 4) / dirs;
     const int64_t most = std::min<int64_t>(nch / (kind == kTc ? 4 : 2), 64);

@@ -486,12 +486,24 @@ __global__ void __launch_bounds__(256) segment_starts_kernel(const GatedProblem 
     const int nch = (gated_unit(p, u).len + chunk - 1) / chunk;
     const float* in = rev ? p.dstate : (p.state ? p.state : p.s0);
     float cur = in ? in[u * usz + e] : 0.f;
-    for (int s = 0; s * p.seg_chunks < nch; ++s) {
-        float* at = p.seg_states + (du * p.segs + s) * usz + e;
-        const bool last = (s + 1) * p.seg_chunks >= nch;
-        const float add = last ? 0.f : *at, decays = last ? 0.f : p.seg_decays[du * p.segs + s];
-        *at = cur;
-        cur = fmaf(decays, cur, add);
+    const int segs = (nch + p.seg_chunks - 1) / p.seg_chunks;
+    float* at = p.seg_states + du * p.segs * usz + e;
+    const float* decay = p.seg_decays + du * p.segs;
+    constexpr int kAhead = 8;  // sums in flight: one after the other, 37 segments took 25 us
+    for (int s0 = 0; s0 < segs; s0 += kAhead) {
+        float add[kAhead], f[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const bool more = s0 + i + 1 < segs;  // (the last has no sum)
+            add[i] = more ? at[static_cast<int64_t>(s0 + i) * usz] : 0.f;
+            f[i] = more ? decay[s0 + i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (s0 + i < segs) {
+                at[static_cast<int64_t>(s0 + i) * usz] = cur;
+                cur = fmaf(f[i], cur, add[i]);
+            }
     }
 }
 
