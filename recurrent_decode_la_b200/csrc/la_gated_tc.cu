@@ -223,7 +223,8 @@ struct StCfg {
                          B_UEMPTY = 4 * NS + NU, B_DONE = 4 * NS + 2 * NU, B_LOEMPTY = B_DONE + 1, B_IFULL = B_LOEMPTY + NL,
                          B_IEMPTY = B_IFULL + kItems, NBAR = B_IEMPTY + kItems;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int OFF_STORED = OFF_MISC + 8;  // chunks stored, a word for each state warp
+    static constexpr int SMEM = OFF_STORED + 4 * NPAN * 4 + 8 + 1024;
     // columns of part k of buffer l (TS)
     static constexpr int tm_part(int l, int k) { return NU * D + (l * 3 + k) * 64; }
     static_assert(SMEM <= 232448, "shared memory");
@@ -237,7 +238,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
     using Cfg = StCfg<D>;
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC);
-    unsigned int* stored = reinterpret_cast<unsigned int*>(smem + Cfg::OFF_MISC + 4);  // parts of states stored so far
+    const uint32_t stored = smem_u32(smem + Cfg::OFF_STORED);
     float* gam = reinterpret_cast<float*>(smem + Cfg::OFF_GAM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.timeout_ns;
@@ -261,7 +262,8 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
             mbar_init(&bar[Cfg::B_IEMPTY + r], 3 + 8 + 4 * Cfg::NPAN);
         }
         *abort_flag = 0;
-        *stored = 0;
+        for (int w = 0; w < 4 * Cfg::NPAN; ++w)
+            reinterpret_cast<volatile unsigned int*>(smem + Cfg::OFF_STORED)[w] = 0;
         fence_barrier_init();
     }
     __syncthreads();
@@ -446,16 +448,19 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
             return true;
         });
     } else if (warp == 3) {
-        // publish a chunk's slot once every part of its state is in global memory
+        // Publish a chunk's slot once every state warp's part of it is in global memory: each warp counts for itself.  (A
+        // sum over the warps would not do: one that has counted the next chunk already makes up for one whose store of this
+        // chunk is still on its way, since a warp lets the next product start before it waits for its store.)
         if (lane == 0 && p.queue != nullptr) {
             walk(kLane, [&](const GatedUnit& un, bool, int c, int, int64_t g, int64_t, bool) {
-                const unsigned int want = static_cast<unsigned int>(g + 1) * (4 * Cfg::NPAN);
-                if (!wait_until(tmo, abort_flag, 0x650, [&] {
-                        unsigned int have;
-                        asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(have) : "r"(smem_u32(stored)) : "memory");
-                        return static_cast<int>(have - want) >= 0;
-                    }))
-                    return false;
+                const unsigned int want = static_cast<unsigned int>(g + 1);
+                for (int w = 0; w < 4 * Cfg::NPAN; ++w)
+                    if (!wait_until(tmo, abort_flag, 0x650, [&] {
+                            unsigned int have;
+                            asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(have) : "r"(stored + 4 * w) : "memory");
+                            return static_cast<int>(have - want) >= 0;
+                        }))
+                        return false;
                 __threadfence();
                 const unsigned int at = atomicAdd(&p.queue[0], 1u);
                 asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.queue + kQueueHead + at),
@@ -579,8 +584,9 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         constexpr int kRows = D / 4;  // rows of this warp
         float S[64];
         int64_t g = 0;
-        auto count_stored = [&] {
-            asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_u32(stored)) : "memory");
+        auto count_stored = [&] {  // this warp's parts of g chunks are in global memory
+            asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(stored + 4 * (warp - 12)), "r"(static_cast<unsigned int>(g))
+                         : "memory");
         };
         items(kWarp, [&](const GatedUnit& un, int64_t u, bool rev, int seg, int nch, int cc0, int cc1) {
             const int64_t item = ((rev ? p.n_units : 0) + u) * p.segs + seg;
@@ -652,7 +658,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
         });
         if (lane == 0) {
             bulk_wait_group<0>();
-            if (g > 0) count_stored();
+            count_stored();
         }
     }
 
