@@ -654,12 +654,15 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                     reinterpret_cast<float4*>(out + at)[j] =
                         make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
             }
+            // The last chunk too, here and not at the next item's first: the publisher waits for it before it looks at another
+            // item, and the items behind may be empty ones, more of them than the producer may be ahead of the publisher.
+            if (lane == 0 && !p.sums) {
+                bulk_wait_group<0>();
+                count_stored();
+            }
             return true;
         });
-        if (lane == 0) {
-            bulk_wait_group<0>();
-            count_stored();
-        }
+        if (lane == 0) bulk_wait_group<0>();
     }
 
     tc_fence_before();

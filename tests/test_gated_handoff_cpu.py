@@ -70,3 +70,56 @@ def test_sum_of_counts_would_publish_early(nu):
     """Why each warp has a count of its own."""
     early, _ = _walk(nu, lambda counts, p: sum(counts) >= (p + 1) * WARPS)
     assert early
+
+
+def _all_published(items, at_end, ring=4):
+    """Whether one CTA's walk ends: items (their chunks) pass from the producer to a state warp and to the publisher through
+    a ring of entries that both have to read.  A chunk is counted when the next one is stored, the last of an item at its
+    end (`at_end`) or, otherwise, behind all items.  No step here disables another, so one order shows all."""
+    made, counted, read = [0], [0], [0, 0]
+
+    def producer():
+        for k in range(len(items) + 1):                       # the last entry says that there are no more
+            while k >= ring and min(read) <= k - ring:
+                yield
+            made[0] = k + 1
+
+    def state_warp():
+        g = 0
+        for k in range(len(items) + 1):
+            while made[0] <= k:
+                yield
+            read[0] = k + 1
+            for _ in range(items[k] if k < len(items) else 0):
+                counted[0] = g                                # those before this one
+                g += 1
+                yield
+            if at_end:
+                counted[0] = g
+        counted[0] = g
+
+    def publisher():
+        g = 0
+        for k in range(len(items) + 1):
+            while made[0] <= k:
+                yield
+            read[1] = k + 1
+            for _ in range(items[k] if k < len(items) else 0):
+                g += 1
+                while counted[0] < g:
+                    yield
+
+    roles = [producer(), state_warp(), publisher()]
+    for _ in range(50 * (len(items) + sum(items) + 1)):
+        roles = [r for r in roles if next(r, "done") != "done"]
+        if not roles:
+            return True
+    return False
+
+
+@pytest.mark.parametrize("empty", range(12))
+def test_a_walk_over_empty_items_ends(empty):
+    for items in ([2] + [0] * empty, [0] * empty + [1], [1] + [0] * empty + [3], [3, 1] + [0] * empty):
+        assert _all_published(items, at_end=True), items
+    if empty >= 4:      # where the last chunk waits for the next one's store
+        assert not _all_published([2] + [0] * empty, at_end=False)

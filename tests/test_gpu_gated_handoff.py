@@ -3,8 +3,9 @@ is read before all of it is there shows in the outputs, in a second call as in t
 import pytest
 import torch
 
+import gated_ref as ref
 import recurrent_decode_la_b200 as la
-from test_gpu_gated import BF16, make, run_backward, run_prefill, ws_for
+from test_gpu_gated import BF16, TOL, TOL_STATE, covered, make, run_backward, run_prefill, ws_for
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,25 @@ def test_long_walks(d):
         assert bool(torch.isfinite(o).all())
         assert _same((o, S), want)
         del o, S
+
+
+EMPTY = {"one walk, then empty ones": [130] + [0] * 40, "few walks": [130, 0, 0, 1, 300] + [0] * 300 + [129],
+         "in segments": [0] * 6 + [1400] + [0] * 2, "unordered": [5, 0, 130] + [0] * 1100 + [1, 200] + [0] * 50, "all empty": [0] * 30}
+
+
+@pytest.mark.parametrize("case", list(EMPTY))
+@pytest.mark.parametrize("d", [64, 128])
+def test_empty_sequences(case, d):
+    """Many more empty sequences than others: a CTA takes many in a row."""
+    lens = EMPTY[case]
+    T = max(sum(lens), 3)
+    x = make(90, BF16, 1, 2, T, d, d, "mild", lens)
+    o, S = run_prefill(x)
+    some = [n for n, m in enumerate(lens) if m]
+    want = x["S0"].view(len(lens), 2, d, d)
+    if some:
+        oo, SS = ref.prefill(x["q"], x["k"], x["v"], x["g"], want[some], [lens[n] for n in some])
+        assert ref.rel(covered(o, lens), oo) <= TOL[BF16]
+        assert ref.rel(S.view(len(lens), 2, d, d)[some], SS.reshape(-1, 2, d, d)) <= TOL_STATE
+    none = [n for n, m in enumerate(lens) if not m]
+    assert torch.equal(S.view(len(lens), 2, d, d)[none], want[none])
