@@ -1030,19 +1030,37 @@ __global__ void __launch_bounds__(640, 1)
     give_tmem(tmem);
 }
 
+// Whether any CTA has claimed a unit of the prefill yet; waits for it, but not longer than it takes the first CTAs of a
+// launch to begin.  Every thread gets the same answer.
+constexpr uint64_t kBeginNs = 20000;
+__device__ __forceinline__ bool walk_begun(const GatedProblem& p) {
+    int begun = 0;
+    if (threadIdx.x == 0) {
+        const uint64_t t0 = globaltimer_ns();
+        do {
+            unsigned int claims;
+            asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(claims) : "l"(p.queue + 3) : "memory");
+            begun = claims != 0;
+        } while (!begun && globaltimer_ns() - t0 < kBeginNs);
+    }
+    return __syncthreads_or(begun) != 0;
+}
+
 // The prefill in one launch: the first n_state CTAs make the states and publish each chunk as its state is stored; the
 // others, and those when they are done, take the chunks in that order.  So K, V and the states come from L2 the second
-// time, and the serial phase of few long sequences overlaps the other.  A CTA waits only for units that CTAs already
-// running have claimed: one of the first takes chunks only when every unit is claimed, and the device starts the others
-// after them.  So it does not matter how many of the CTAs are on the device at once.  (Roles by order of arrival at a
-// counter instead of by index: 445 us, not 362, at B8 H16 T8192, since the first to arrive sit close together.)
+// time, and the serial phase of few long sequences overlaps the other.
+// A CTA takes chunks, and so may wait for them, only after it has seen a unit claimed: whoever claimed it is running, waits
+// for nobody and claims on until no unit is left.  A CTA that sees none claimed makes states itself.  So it matters neither
+// how many of the CTAs are on the device at once nor in which order they start.  (Roles by order of arrival at a counter
+// instead of by index: 445 us, not 362, at B8 H16 T8192, since the first to arrive sit close together.)
 template <int D>
 __global__ void __launch_bounds__(640, 1)
     gated_prefill_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items, int n_state) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = aligned_smem(smem_raw);
     const uint32_t tmem = take_tmem(smem);
-    if (static_cast<int>(blockIdx.x) < n_state) gated_states_body<D>(m, p, n_items, false, smem, tmem, blockIdx.x, n_state);
+    if (static_cast<int>(blockIdx.x) < n_state || !walk_begun(p))
+        gated_states_body<D>(m, p, n_items, false, smem, tmem, blockIdx.x, n_state);
     gated_out_body<D>(m, p, smem, tmem);
     give_tmem(tmem);
 }

@@ -3,7 +3,11 @@
 A state warp, for every chunk g: issue the store of its part of the state, wait until its store of chunk g - 1 has
 landed and count that, wait for the product of chunk g (which starts when every warp has read accumulator g - NU), read
 it, and let the next product start.  Behind the last chunk it waits for all its stores and counts them.  Stores land in
-any order that the waits allow.  The publisher releases chunk 0, 1, .. as the counts permit."""
+any order that the waits allow.  The publisher releases chunk 0, 1, .. as the counts permit.
+
+And the roles of the launch's CTAs, under every order in which they may start on a device with room for some of them."""
+import itertools
+
 import pytest
 
 CHUNKS, WARPS = 4, 2
@@ -123,3 +127,34 @@ def test_a_walk_over_empty_items_ends(empty):
         assert _all_published(items, at_end=True), items
     if empty >= 4:      # where the last chunk waits for the next one's store
         assert not _all_published([2] + [0] * empty, at_end=False)
+
+
+def _finishes(order, room, makers, units, look):
+    """Whether the launch ends: CTAs start in this order while there is room.  A maker claims and walks every unit left and
+    waits for nobody; a consumer takes the chunks (one a unit) in turn and waits for each.  With `look` a CTA makes states
+    too if no unit has been claimed when it starts."""
+    todo, waiting = list(order), []          # waiting: the chunks that the resident CTAs wait for
+    walked = taken = 0
+    while True:
+        waiting = [c for c in waiting if c >= walked]
+        while taken < walked:                # whoever is not waiting takes what is there
+            taken += 1
+        if taken >= units and not waiting:
+            return True
+        if not todo or len(waiting) >= room:
+            return False
+        cta = todo.pop(0)
+        if cta < makers or (look and walked == 0):
+            walked = units
+        else:
+            waiting.append(taken)
+            taken += 1
+
+
+@pytest.mark.parametrize("room", [1, 2, 3])
+@pytest.mark.parametrize("makers", [1, 2])
+def test_every_start_order_finishes(room, makers):
+    orders = list(itertools.permutations(range(5)))
+    assert all(_finishes(o, room, makers, 6, look=True) for o in orders)
+    # by index alone, a device full of consumers would wait until they give up
+    assert not all(_finishes(o, room, makers, 6, look=False) for o in orders)
