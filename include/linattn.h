@@ -157,7 +157,7 @@ la_status la_decode_step(const void* q, const void* k, const void* v, void* o,
  * with one log gate g_t per token and head (g_t <= 0 decays, 0 keeps, -inf
  * starts afresh).  g is [B, H, T] ([1, H, T_total] packed, [B, H] for one
  * token) in `dtype`; NULL means no decay, the recurrence of la_prefill.
- * Gates below -110 decay by exactly zero.  Positive gates are taken as they
+ * Gates below -110 count as -110, which decays to zero.  Positive gates are taken as they
  * are while the sum of those of any 128 tokens stays below 80.
  * Inputs are finite apart from gates of -inf: a NaN or infinity in q, k, v or
  * a gradient may reach every token of the chunk of 128 that holds it.
@@ -211,7 +211,10 @@ const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens,
  *   dstate: [units][d_k][d_v] float32, updated in place: the gradient of S_T
  *     on entry, of S_0 on return (an empty sequence leaves it as it is).
  *   dq, dk, dv, dg: gradients of q, k, v and g, written, in `dtype`; dg may be
- *     NULL.  The gradient of a gate that decays to zero is zero.
+ *     NULL.  The gradient of a gate of -110 or less is zero.  "tc" takes dg
+ *     from sums over the chunk of 128 tokens in which terms cancel: where a
+ *     gate lets little through, dg is off by fp32 of the size of those terms
+ *     (q . dq, k . dk), not of its own.
  *   workspace: la_gated_prefill_backward_workspace_size() bytes, as above.
  * Nothing is taken from the forward call but its inputs: the states are made
  * again.  Results do not depend on any order of execution.  Errors as for

@@ -427,6 +427,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_simt_kernel(const GatedPr
         if (lane < 8) s = fmaf(decay(G[C - 1]), es[lane], s);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        // nothing passes a gate at the floor, whatever positive gates follow it
+        if (__shfl_sync(0xffffffffu, gv, t) <= kGateFloor) s = 0.f;
         if (lane == 0) st1(static_cast<T*>(p.dg), ch.row0 + t, s);
     }
 }

@@ -1075,9 +1075,10 @@ __global__ void __launch_bounds__(640, 1)
 // accumulated onto it.  dg comes from the results, before they are rounded:
 // with cj = e^{G_C - G_j} k_j . (E v_j), taken when T3 is scaled,
 //     dg_t = e^{G_C} <E, S> + sum_{i >= t} (q_i . dq_i - k_i . dk_i + cj_i) + sum_{j < t} cj_j.
-// Within the chunk dq and dk are sums of the same rounded W_ij, so what a
-// token gives and what it takes cancel to fp32, and the sums restart at every
-// chunk.
+// The pairs on one side of gate t are in both sums and cancel: dq and dk are
+// sums of the same rounded W_ij, so they do to fp32 of their size, over the 128
+// tokens of a chunk at most.  That is dg's error where a gate lets little
+// through; behind one that lets nothing through dg is set to zero.
 //   warp 0       producer            warp 1  MMA issuer
 //   warp 2       decays; zeroes the rows behind a sequence's end; stores dv
 //   warp 3       dg; stores dq and dk
@@ -1396,6 +1397,19 @@ __global__ void __launch_bounds__(640, 1)
         walk([&](const GatedChunk& ch, int64_t, int64_t g) {
             const int s = static_cast<int>(g % Cfg::NS);
             const uint32_t gp = static_cast<uint32_t>(g & 1);
+            // a gate at the floor, or one that no path of the chunk crosses with a weight of 2^-126, even with all of its
+            // positive gates
+            bool closed[4];
+            {
+                float x[4], up = 0.f;
+                load_gates(p, ch.row0, ch.nv, x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) up += fmaxf(x[e], 0.f);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) up += __shfl_xor_sync(0xffffffffu, up, o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) closed[e] = x[e] <= kGateFloor * kLog2e || x[e] + up < -126.f;
+            }
             auto store = [&](int n, int tile, const CUtensorMap* map) {
                 if (!mbar_wait_warp(&bar[Cfg::B_STAGED + n], gp, abort_flag, tmo, 0x832 + n)) return false;
                 if (lane == 0 && ch.nv == C) store_tile<D>(map, smem + s * Cfg::STAGE + tile * Cfg::TILE, ch);
@@ -1443,7 +1457,8 @@ __global__ void __launch_bounds__(640, 1)
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.dg) + ch.row0 + 4 * lane;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (4 * lane + e < ch.nv) out[e] = __float2bfloat16_rn(e0 + after[e] + u[e] + (upto[e] - d[e]));
+                    if (4 * lane + e < ch.nv)
+                        out[e] = __float2bfloat16_rn(closed[e] ? 0.f : e0 + after[e] + u[e] + (upto[e] - d[e]));
             }
             return true;
         });
