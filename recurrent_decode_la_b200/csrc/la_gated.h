@@ -98,6 +98,9 @@ __device__ __forceinline__ GatedUnit gated_unit(const GatedProblem& p, int64_t u
     return {h * p.rows + a, h * p.nc + p.choff[n], b - a};
 }
 
+// Chunks of C tokens in len (len + C - 1 need not fit an int).
+__host__ __device__ constexpr int gated_chunks(int len, int C) { return len / C + (len % C != 0 ? 1 : 0); }
+
 struct GatedChunk {
     int64_t row0;  // first row of the chunk in the [groups][rows] token layout
     int group;

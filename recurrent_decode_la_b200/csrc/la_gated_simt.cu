@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
     const float* in = rev ? p.dstate + u * usz : (p.state ? p.state + u * usz : (p.s0 ? p.s0 + u * usz : nullptr));
     float* out = rev ? p.dstate + u * usz : (p.state ? p.state + u * usz : nullptr);
     float* slots = static_cast<float*>(rev ? p.e_states : p.s_states);
-    const int nch = (un.len + C - 1) / C;
+    const int nch = gated_chunks(un.len, C);
     const int cc0 = seg * p.seg_chunks, cc1 = min(nch, cc0 + p.seg_chunks);
     if (cc0 >= cc1 || (p.sums && cc1 == nch)) return;  // (nothing starts from the last one's sum)
     if (p.segs > 1) {
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __re
         int32_t x = 0;
         if (n < num_seqs) {
             const int a = cu[n], b = cu[n + 1];
-            if (!(a < 0 || b < a || static_cast<int64_t>(b) > rows)) x = (b - a + chunk - 1) / chunk;
+            if (!(a < 0 || b < a || static_cast<int64_t>(b) > rows)) x = gated_chunks(b - a, chunk);
             if (order != nullptr) chunks[n] = x;
         }
         int64_t s = x;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(256) segment_starts_kernel(const GatedProblem 
     if (e >= usz) return;
     const bool rev = du >= p.n_units;
     const int64_t u = du - (rev ? p.n_units : 0);
-    const int nch = (gated_unit(p, u).len + chunk - 1) / chunk;
+    const int nch = gated_chunks(gated_unit(p, u).len, chunk);
     const float* in = rev ? p.dstate : (p.state ? p.state : p.s0);
     float cur = in ? in[u * usz + e] : 0.f;
     const int segs = (nch + p.seg_chunks - 1) / p.seg_chunks;

@@ -313,7 +313,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
             int64_t u = grad ? i >> 1 : i;
             if (p.order != nullptr) u = static_cast<int64_t>(p.order[u / p.H]) * p.H + u % p.H;
             const GatedUnit un = gated_unit(p, u);
-            const int nch = (un.len + C - 1) / C, cc0 = seg * p.seg_chunks, cc1 = min(nch, cc0 + p.seg_chunks);
+            const int nch = gated_chunks(un.len, C), cc0 = seg * p.seg_chunks, cc1 = min(nch, cc0 + p.seg_chunks);
             if (cc0 >= cc1 || (p.sums && cc1 == nch)) continue;  // (nothing starts from the last one's sum)
             if (!f(un, u, rev, seg, nch, cc0, cc1)) return false;
         }
@@ -357,7 +357,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 }
                 started = g + 1;
                 const int c2 = rev ? c - 1 : c + 1;
-                if (c2 >= 0 && c2 * C < un.len) {
+                if (c2 >= 0 && c2 < gated_chunks(un.len, C)) {
                     coords(un, c2, row, group);
 #pragma unroll
                     for (int pn = 0; pn < Cfg::NPAN; ++pn) {
