@@ -156,7 +156,8 @@ la_status la_decode_step(const void* q, const void* k, const void* v, void* o,
  *       S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = q_t^T S_t
  * with one log gate g_t per token and head (g_t <= 0 decays, 0 keeps, -inf
  * starts afresh).  g is [B, H, T] ([1, H, T_total] packed, [B, H] for one
- * token) in `dtype`; NULL means no decay, the recurrence of la_prefill.
+ * token) in `dtype`; NULL means no decay, the recurrence of la_prefill (which
+ * computes it in half the time and without a workspace).
  * Gates below -110 count as -110, which decays to zero.  Positive gates are taken as they
  * are while the sum of those of any 128 tokens stays below 80.
  * Inputs are finite apart from gates of -inf: a NaN or infinity in q, k, v or

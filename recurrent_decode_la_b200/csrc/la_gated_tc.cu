@@ -17,20 +17,28 @@
 // V and that of the states hit L2 (B2 H16 T4096), twice that when the states run
 // further ahead than L2 reaches (B8 H16 T4096: 1032 MB in 196 us, 80 % of the copy
 // rate; evict-first policies on the second readings changed nothing).  B8 H16
-// T8192: 372 us on a cool device and 415 in a long run; the floor of its bytes is
-// 167.  The gradient moves 955 MB at B4 H16 T4096 where 483 are the least: both
+// T8192: 420 to 440 us in a long run; the floor of its bytes is 167, and the
+// ungated prefill, which walks a unit and makes its outputs in one CTA and reads
+// every byte once, takes 215.  (Times that compare two forms below were taken in
+// turn in short runs, where this case takes 370.)  The gradient moves 955 MB at B4 H16 T4096 where 483 are the least: both
 // states at 72 % of the copy rate (145 us of B4 H16 T8192), then the chunks at
 // 58 %, each a chain of seven products and the steps between them that takes a CTA
-// 16k clocks (272 us); in all 440 to 480 us, floor 145.
+// 16k clocks (272 us); in all 455 to 475 us, floor 145.
 //
 // Rounding.  Sums, states and decays are fp32.  An operand of a product is
 // rounded to bf16 once where its result is bf16 too (decayed scores, chunk
 // states).  Where the result is an fp32 state, the decayed keys (queries) are
 // kept as the sum of three bf16 numbers, 2^-24 of them, at the price of two
 // more products (two parts would leave the state 2.4e-6 of itself off, three
-// 1e-7).  A row's decay is applied to the fp32 accumulator, not to a bf16 operand.  The tensor core drops bits when it adds to an accumulator: a state
-// summed there over 8192 tokens is off by 9e-6 of itself, so the states live in
-// registers and an accumulator spans one chunk only.
+// 1e-7).  A row's decay is applied to the fp32 accumulator, not to a bf16 operand.
+// dg's term e^{G_C} <E, S>, the same for all tokens of a chunk, is an fp32 sum over
+// the chunk's two rounded states, since the fp32 ones are in two CTAs and nowhere at
+// once: where it outweighs the others and its products nearly cancel, dg is further
+// off than dq, dk and dv (single units of 20 tokens: 0.0028 on average and up to
+// 0.009, the others 0.0024; 500 tokens: all alike).
+// The tensor core drops bits when it adds to an accumulator: a state summed there
+// over 8192 tokens is off by 9e-6 of itself, so the states live in registers and an
+// accumulator spans one chunk only.
 //
 // Waits are bounded: on expiry the kernel records the device error word, every
 // role winds down, copies and products in flight are drained (bounded), tensor
