@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_simt_kernel(const GatedPr
     float* P = W + C * kLdC;      // w_ij (q_i . k_j)
     float* ri = P + C * kLdC;     // e^{G_i} q_i . (S do_i)
     float* cj = ri + C;           // e^{G_C - G_j} k_j . (E v_j)
-    float* es = cj + C;           // per-warp sums of <E, S>
+    float* es = cj + C;           // per-warp sums of e^{G_C} <E, S>
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const GatedChunk ch = gated_chunk(p, blockIdx.x, C);
     if (ch.nv <= 0) return;
@@ -360,10 +360,14 @@ __global__ void __launch_bounds__(kThreads) gated_grad_simt_kernel(const GatedPr
         W[r * kLdC + lane] = lane <= r ? wij * b[i] : 0.f;
         mij[i] = lane < r ? wij * a[i] * b[i] : 0.f;
     }
+    // e^{G_C} <E, S>, half of the decay on either side: behind a memory that grew, ahead of one that will, E S alone may
+    // leave float32
     float part = 0.f;
+    const float half = decay(G[C - 1]) == 0.f ? 0.f : decay(0.5 * G[C - 1]);
     for (int r = w; r < dk; r += 8)
 #pragma unroll
-        for (int m = 0; m < NM; ++m) part = fmaf(S[r * LD + lane + 32 * m], E[r * LD + lane + 32 * m], part);
+        for (int m = 0; m < NM; ++m)
+            part = fmaf(half * S[r * LD + lane + 32 * m], half * E[r * LD + lane + 32 * m], part);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == 0) es[w] = part;
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_simt_kernel(const GatedPr
         } else if (lane < nv) {
             s = ri[lane];
         }
-        if (lane < 8) s = fmaf(decay(G[C - 1]), es[lane], s);
+        if (lane < 8) s += es[lane];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         // nothing passes a gate at the floor, whatever positive gates follow it

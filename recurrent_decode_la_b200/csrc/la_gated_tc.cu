@@ -1588,24 +1588,27 @@ __global__ void __launch_bounds__(640, 1)
             tmem_wait_st();
             tc_fence_before();
             arrive(Cfg::B_ZS);
-            // e^{G_C} <E, S>, a share of the elements per thread
+            // e^{G_C} <E, S>, a share of the elements per thread; half of the decay on either side: behind a memory that grew,
+            // ahead of one that will, E S alone may leave fp32
             {
-                float acc = 0.f;
+                float2 sum = make_float2(0.f, 0.f);
+                const float half = Pre[C - 1] == 0.f ? 0.f : ex2(0.5f * G[C - 1]);
+                const float2 hh = make_float2(half, half);
 #pragma unroll 2
                 for (int i = (threadIdx.x - 128) * 16; i < Cfg::SB; i += 512 * 16) {
                     uint32_t a[4], b[4];
                     ld_shared_v4(st + Cfg::S + i, a[0], a[1], a[2], a[3]);
                     ld_shared_v4(st + Cfg::E + i, b[0], b[1], b[2], b[3]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        acc = fmaf(bf16_lo(a[e]), bf16_lo(b[e]), acc);
-                        acc = fmaf(bf16_hi(a[e]), bf16_hi(b[e]), acc);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        sum = __ffma2_rn(__fmul2_rn(hh, make_float2(bf16_lo(a[e]), bf16_hi(a[e]))),
+                                         __fmul2_rn(hh, make_float2(bf16_lo(b[e]), bf16_hi(b[e]))), sum);
                 }
+                float acc = sum.x + sum.y;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
                 if (lane == 0) {
-                    es[warp - 4] = Pre[C - 1] * acc;
+                    es[warp - 4] = acc;
                     mbar_arrive(empty(s, Cfg::F_S));
                     mbar_arrive(empty(s, Cfg::F_E));
                 }
