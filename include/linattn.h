@@ -160,6 +160,8 @@ la_status la_decode_step(const void* q, const void* k, const void* v, void* o,
  * computes it in half the time and without a workspace).
  * Gates below -110 count as -110, which decays to zero.  Positive gates are taken as they
  * are while the sum of those of any 128 tokens stays below 80.
+ * A stretch of gates that decays below 2^-126 may count as zero, whatever
+ * positive gates follow it.
  * Inputs are finite apart from gates of -inf: a NaN or infinity in q, k, v or
  * a gradient may reach every token of the chunk of 128 that holds it.
  * Outputs may not overlap inputs, other than where a parameter is said to be

@@ -66,7 +66,8 @@ struct GatedProblem {
     unsigned int* queue;
     // Segments of a unit's walk (few long units): segs runs of seg_chunks chunks, each walked by itself.  A first pass
     // (sums) makes what each adds to a state of zero, with its decay; their prefix gives each one's start; the second
-    // pass goes on from there.  seg_states [directions][units][segs][d_k][d_v], seg_decays [directions][units][segs].
+    // pass goes on from there.  seg_states [directions][units][segs][d_k][d_v], seg_decays [directions][units][segs], as
+    // powers of two (positive gates may let a segment grow by more than fp32 holds).
     int segs;
     int seg_chunks;
     bool sums;

@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
         in = p.sums ? nullptr : start;
         out = p.sums ? start : (cc1 == nch ? out : nullptr);
     }
-    float S[4][4], whole = 1.f;
+    float S[4][4];
+    double whole = 0.0;  // log gates of the segment
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
         for (int i = 0; i < C / 8; ++i) Y[yr + 8 * i][yc] = yv[i] * __shfl_sync(0xffffffffu, wt, yr + 8 * i);
         __syncthreads();
         if (cc + 1 < cc1) fetch(cc + 1);
-        whole *= gamma;
+        whole += all;
         float* slot = slots + (un.slot0 + c) * usz;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) gated_states_simt_kernel(const Gated
                 for (int m = 0; m < 4; ++m) S[i][m] = fmaf(xa[i], ya[m], S[i][m]);
         }
     }
-    if (p.sums && blockIdx.x % col_blocks == 0 && tid == 0) p.seg_decays[item] = whole;
+    if (p.sums && blockIdx.x % col_blocks == 0 && tid == 0) p.seg_decays[item] = static_cast<float>(whole * 1.4426950408889634);
     if (out) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -480,6 +481,13 @@ __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __re
     }
 }
 
+// x 2^e.  Beyond 2^+-300 nothing of a float is left but zero or infinity.
+__device__ __forceinline__ float times_power(float x, float e) {
+    e = fminf(fmaxf(e, -300.f), 300.f);
+    const float n = rintf(e);
+    return scalbnf(x * exp2f(e - n), static_cast<int>(n));
+}
+
 // One thread per element of a unit's state: walks the unit's segments.
 __global__ void __launch_bounds__(256) segment_starts_kernel(const GatedProblem p, int chunk, int usz) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -508,7 +516,7 @@ __global__ void __launch_bounds__(256) segment_starts_kernel(const GatedProblem 
         for (int i = 0; i < kAhead; ++i)
             if (s0 + i < segs) {
                 at[static_cast<int64_t>(s0 + i) * usz] = cur;
-                cur = fmaf(f[i], cur, add[i]);
+                cur = times_power(cur, f[i]) + add[i];
             }
     }
 }

@@ -449,7 +449,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
             if (lane == 0) gam[g % Cfg::kGam] = ex2(all);
             if (p.sums) {
                 decay = first ? all : decay + all;
-                if (lane == 0) p.seg_decays[item] = ex2(decay);
+                if (lane == 0) p.seg_decays[item] = decay;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_GFULL + s]);

@@ -25,3 +25,21 @@ def test_growth_and_valley(dtype, dk, dv, where):
     for name, a, b in zip(("o", "S", "dq", "dk", "dv", "dg", "dS0"), got, want):
         err = ref.rel(a, b)
         assert err <= (TOL_STATE if name in ("S", "dS0") else TOL[dtype]), (name, err)
+
+
+@pytest.mark.parametrize("dtype,dk,dv,T,rise", [(BF16, 64, 64, 2200, (640, 1280, 0.15)), (BF16, 128, 128, 2200, (640, 1280, 0.15)),
+                                                (F32, 8, 8, 16384, (8192, 8448, 0.4))])
+def test_growth_over_a_segment(dtype, dk, dv, T, rise):
+    """A segment of the walk that grows by e^96 and e^102, and small values for it.  The exponents, up to 148 powers of two,
+    are float32 sums on the tensor cores: 20 roundings of at most 2^-18 each put e^x at most 20 * 2^-18 * ln 2 < 2^-14 off."""
+    x = make(112, dtype, 1, 2, T, dk, dv)
+    for m in ("v", "do", "S0", "dS"):
+        x[m] *= 1e-12
+    a, b, g = rise
+    x["g"][:, :, a:b] = g
+    args = [x[m] for m in ("q", "k", "v", "g")]
+    got = [*run_prefill(x), *run_backward(x)]
+    want = [*ref.prefill(*args, x["S0"]), *ref.prefill_backward(*args, x["S0"], x["do"], x["dS"])]
+    for name, u, w in zip(("o", "S", "dq", "dk", "dv", "dg", "dS0"), got, want):
+        err = ref.rel(u, w)
+        assert err <= (2 * TOL_STATE if name in ("S", "dS0") else TOL[dtype]), (name, err)
