@@ -203,7 +203,7 @@ size_t la_gated_prefill_workspace_size(la_dtype dtype, int B, int H, int64_t T,
 
 /* Which kernel la_gated_prefill runs: max_tokens is T for dense input and
  * max_seqlen for packed input.  "short", "tc", "simt" or "unsupported".  Host
- * only.  The gradient has no "short" kernel. */
+ * only.  (Of the gradient's: see there.) */
 const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens,
                                     int d_k, int d_v);
 
@@ -219,8 +219,10 @@ const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens,
  *     gate lets little through, dg is off by fp32 of the size of those terms
  *     (q . dq, k . dk), not of its own.
  *   workspace: la_gated_prefill_backward_workspace_size() bytes, as above.
+ * Kernels: those of la_gated_prefill, but "short", and "simt" for at most 32
+ * tokens of at most 32 units (dense) of any size.
  * Nothing is taken from the forward call but its inputs: the states are made
- * again.  Results do not depend on any order of execution.  Errors as for
+ * again.  dq holds intermediate values until the call's work has finished.  Results do not depend on any order of execution.  Errors as for
  * la_gated_prefill. */
 la_status la_gated_prefill_backward(const void* q, const void* k,
                                     const void* v, const void* g,

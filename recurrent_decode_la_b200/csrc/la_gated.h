@@ -107,6 +107,7 @@ struct GatedChunk {
     int group;
     int row;  // row0 = group * rows + row
     int nv;   // its tokens; 0: the slot holds no chunk
+    bool alone;  // its unit's only one
 };
 
 constexpr int kQueueHead = 4;
@@ -118,19 +119,20 @@ __device__ __forceinline__ GatedChunk gated_chunk(const GatedProblem& p, int64_t
     if (p.cu == nullptr) {
         const int64_t r = static_cast<int64_t>(ci) * C;
         const int64_t left = p.rows - r;
-        return {group * p.rows + r, static_cast<int>(group), static_cast<int>(r), static_cast<int>(left < C ? left : C)};
+        return {group * p.rows + r, static_cast<int>(group), static_cast<int>(r), static_cast<int>(left < C ? left : C), p.rows <= C};
     }
-    if (ci >= p.choff[p.num_seqs]) return {0, 0, 0, 0};
+    if (ci >= p.choff[p.num_seqs]) return {0, 0, 0, 0, false};
     int lo = 0, hi = p.num_seqs - 1;  // the last sequence with choff[n] <= ci
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (p.choff[mid] <= ci) lo = mid; else hi = mid - 1;
     }
-    if (p.choff[lo + 1] > p.nc) return {0, 0, 0, 0};
+    if (p.choff[lo + 1] > p.nc) return {0, 0, 0, 0, false};
     const int c = ci - p.choff[lo];
     const int64_t a = p.cu[lo] + static_cast<int64_t>(c) * C;
     const int64_t left = p.cu[lo + 1] - a;
-    return {group * p.rows + a, static_cast<int>(group), static_cast<int>(a), static_cast<int>(left < C ? left : C)};
+    return {group * p.rows + a, static_cast<int>(group), static_cast<int>(a), static_cast<int>(left < C ? left : C),
+            p.choff[lo + 1] - p.choff[lo] == 1};
 }
 
 // choff[n] = chunks of C tokens in the sequences before n (offsets out of

@@ -31,11 +31,14 @@
 // kept as the sum of three bf16 numbers, 2^-24 of them, at the price of two
 // more products (two parts would leave the state 2.4e-6 of itself off, three
 // 1e-7).  A row's decay is applied to the fp32 accumulator, not to a bf16 operand.
-// dg's term e^{G_C} <E, S>, the same for all tokens of a chunk, is an fp32 sum over
-// the chunk's two rounded states, since the fp32 ones are in two CTAs and nowhere at
-// once: where it outweighs the others and its products nearly cancel, dg is further
-// off than dq, dk and dv (single units of 20 tokens: 0.0028 on average and up to
-// 0.009, the others 0.0024; 500 tokens: all alike).
+// dg's term e^{G_C} <E, S>, the same for all tokens of a chunk, is an fp32 sum: over
+// the fp32 states of a unit's only chunk (summed where the states are made; the
+// rounded ones put dg of 32 units of 1 token 0.0029 off, so 0.0017), but over the
+// rounded ones of a longer unit's chunks, since their fp32 ones are in two CTAs and
+// nowhere at once.  Where that outweighs the other terms and its products nearly
+// cancel, dg is further off than dq, dk and dv (one unit of 150 to 500 tokens: 0.0024
+// on average and up to 0.0042, the others 0.0025).  With the next eight bits of
+// either state beside it the gradient of B4 H16 T8192 took 639 us, not 460.
 // The tensor core drops bits when it adds to an accumulator: a state summed there
 // over 8192 tokens is off by 9e-6 of itself, so the states live in registers and an
 // accumulator spans one chunk only.
@@ -129,6 +132,13 @@ __device__ __forceinline__ void scan_down(const float (&x)[4], float (&B)[4], fl
 #pragma unroll
     for (int e = 0; e < 4; ++e) B[e] += behind;
     all = __shfl_sync(0xffffffffu, s, 0);
+}
+
+// Where the states' kernel of the gradient leaves e^{G_C} <E, S_0> of a unit's only chunk for the chunks' kernel, a number
+// a state warp: the row of dq that the chunk's first token will take.
+template <int D>
+__device__ __forceinline__ float* alone_sums(const GatedProblem& p, int64_t row0) {
+    return reinterpret_cast<float*>(static_cast<uint16_t*>(p.dq) + row0 * D);
 }
 
 // Zero rows nv .. 127 of a [128][D] tile (one warp).
@@ -645,6 +655,24 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) return false;
                 tc_fence_after();
                 const float gamma = gam[g % Cfg::kGam];
+                if (grad && rev && nch == 1) {
+                    // The unit's only chunk: its states, E and S_0, are both at hand in fp32.  Half of the decay on either side.
+                    float dot = 0.f;
+                    const float half_decay = sqrtf(gamma);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (p.s0 != nullptr && row >= 0) x = reinterpret_cast<const float4*>(p.s0 + at)[j];
+                        dot = fmaf(half_decay * x.x, half_decay * S[4 * j], dot);
+                        dot = fmaf(half_decay * x.y, half_decay * S[4 * j + 1], dot);
+                        dot = fmaf(half_decay * x.z, half_decay * S[4 * j + 2], dot);
+                        dot = fmaf(half_decay * x.w, half_decay * S[4 * j + 3], dot);
+                        __syncwarp();  // one load at a time: sixteen would take the registers of S
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                    if (lane == 0) alone_sums<D>(p, un.row0)[warp - 12] = dot;
+                }
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     float x[16];
@@ -766,7 +794,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
             if (!one) __syncwarp();
             if (lane == 0) mbar_arrive(&bar[Cfg::B_UEMPTY + r]);
             if (nv <= 0) return true;
-            if (!f(GatedChunk{group * p.rows + row, group, row, nv}, g)) return false;
+            if (!f(GatedChunk{group * p.rows + row, group, row, nv, false}, g)) return false;
         }
     };
 
@@ -779,7 +807,7 @@ __device__ __forceinline__ void gated_out_body(const GatedMaps& m, const GatedPr
                     // the next chunk in the order in which the states come to be
                     const unsigned int at = atomicAdd(&p.queue[1], 1u);
                     unsigned int entry = 0;
-                    GatedChunk ch = {0, 0, 0, 0};
+                    GatedChunk ch = {0, 0, 0, 0, false};
                     if (at < total) {
                         if (!wait_until(tmo, abort_flag, 0x772, [&] {
                                 asm volatile("ld.acquire.gpu.global.u32 %0, [%1];"
@@ -1423,6 +1451,8 @@ __global__ void __launch_bounds__(640, 1)
                 if (lane == 0 && ch.nv == C) store_tile<D>(map, smem + s * Cfg::STAGE + tile * Cfg::TILE, ch);
                 return true;
             };
+            // what lies in dq's first row is read (every warp gives S back behind that)
+            if (ch.alone && !mbar_wait_warp(empty(s, Cfg::F_S), (g / Cfg::NS) & 1, abort_flag, tmo, 0x835)) return false;
             if (!store(0, Cfg::F_Q, &m.dq) || !store(1, Cfg::F_K, &m.dk)) return false;
             if (lane == 0) {  // hand each tile back as soon as its store has read it
                 if (ch.nv == C) bulk_wait_group_read<1>();
@@ -1595,7 +1625,7 @@ __global__ void __launch_bounds__(640, 1)
                 const float half = Pre[C - 1] == 0.f ? 0.f : ex2(0.5f * G[C - 1]);
                 const float2 hh = make_float2(half, half);
 #pragma unroll 2
-                for (int i = (threadIdx.x - 128) * 16; i < Cfg::SB; i += 512 * 16) {
+                for (int i = (threadIdx.x - 128) * 16; i < Cfg::SB && !ch.alone; i += 512 * 16) {
                     uint32_t a[4], b[4];
                     ld_shared_v4(st + Cfg::S + i, a[0], a[1], a[2], a[3]);
                     ld_shared_v4(st + Cfg::E + i, b[0], b[1], b[2], b[3]);
@@ -1608,6 +1638,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
                 if (lane == 0) {
+                    if (ch.alone) acc = warp < 4 + 4 * Cfg::NPAN ? alone_sums<D>(p, ch.row0)[warp - 4] : 0.f;
                     es[warp - 4] = acc;
                     mbar_arrive(empty(s, Cfg::F_S));
                     mbar_arrive(empty(s, Cfg::F_E));
@@ -1637,6 +1668,8 @@ __global__ void __launch_bounds__(640, 1)
                 return sum;
             };
             if (!wait(Cfg::B_DK, gp, 0x850)) return false;
+            // before any row is written: what lies in dq's first one is read
+            if (ch.alone && !wait(Cfg::B_EMPTY + 6 * s + Cfg::F_S, ph, 0x852)) return false;
             tc_fence_after();
             float u = 0.f;
 #pragma unroll 1
