@@ -481,13 +481,6 @@ __global__ void __launch_bounds__(1024) chunk_offsets_kernel(const int32_t* __re
     }
 }
 
-// x 2^e.  Beyond 2^+-300 nothing of a float is left but zero or infinity.
-__device__ __forceinline__ float times_power(float x, float e) {
-    e = fminf(fmaxf(e, -300.f), 300.f);
-    const float n = rintf(e);
-    return scalbnf(x * exp2f(e - n), static_cast<int>(n));
-}
-
 // One thread per element of a unit's state: walks the unit's segments.
 __global__ void __launch_bounds__(256) segment_starts_kernel(const GatedProblem p, int chunk, int usz) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -512,11 +505,14 @@ __global__ void __launch_bounds__(256) segment_starts_kernel(const GatedProblem 
             add[i] = more ? at[static_cast<int64_t>(s0 + i) * usz] : 0.f;
             f[i] = more ? decay[s0 + i] : 0.f;
         }
+        // half of the decay, applied twice: a segment's may leave float32 (beyond 2^+-250 nothing of a state would be left)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) f[i] = exp2f(0.5f * fminf(fmaxf(f[i], -250.f), 250.f));
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (s0 + i < segs) {
                 at[static_cast<int64_t>(s0 + i) * usz] = cur;
-                cur = times_power(cur, f[i]) + add[i];
+                cur = fmaf(f[i] * cur, f[i], add[i]);
             }
     }
 }

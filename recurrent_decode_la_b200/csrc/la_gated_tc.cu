@@ -249,8 +249,9 @@ struct StCfg {
 };
 
 // `worker` of `workers` CTAs; smem 1 KB aligned, tmem all 512 columns.  With p.queue (prefill) the slots are published as
-// their states are stored.
-template <int D>
+// their states are stored.  ALONE: units of one chunk may be among them (their sums for dg are made here; that takes
+// registers, which others need not pay for).
+template <int D, bool ALONE>
 __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const GatedProblem& p, int64_t n_items, bool grad,
                                                   uint8_t* smem, uint32_t tmem, int64_t worker, int64_t workers) {
     using Cfg = StCfg<D>;
@@ -655,7 +656,7 @@ __device__ __forceinline__ void gated_states_body(const GatedMaps& m, const Gate
                 if (!mbar_wait_warp(&bar[Cfg::B_UFULL + b], (g / Cfg::NU) & 1, abort_flag, tmo, 0x640 + b)) return false;
                 tc_fence_after();
                 const float gamma = gam[g % Cfg::kGam];
-                if (grad && rev && nch == 1) {
+                if (ALONE && rev && nch == 1) {
                     // The unit's only chunk: its states, E and S_0, are both at hand in fp32.  Half of the decay on either side.
                     float dot = 0.f;
                     const float half_decay = sqrtf(gamma);
@@ -1056,13 +1057,13 @@ __device__ __forceinline__ void give_tmem(uint32_t tmem) {
 }
 
 // The states of the gradient, both directions; the sums of segments.
-template <int D>
+template <int D, bool ALONE>
 __global__ void __launch_bounds__(640, 1)
     gated_states_tc_kernel(const __grid_constant__ GatedMaps m, const GatedProblem p, int64_t n_items, bool grad) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = aligned_smem(smem_raw);
     const uint32_t tmem = take_tmem(smem);
-    gated_states_body<D>(m, p, n_items, grad, smem, tmem, blockIdx.x, gridDim.x);
+    gated_states_body<D, ALONE>(m, p, n_items, grad, smem, tmem, blockIdx.x, gridDim.x);
     give_tmem(tmem);
 }
 
@@ -1096,7 +1097,7 @@ __global__ void __launch_bounds__(640, 1)
     uint8_t* smem = aligned_smem(smem_raw);
     const uint32_t tmem = take_tmem(smem);
     if (static_cast<int>(blockIdx.x) < n_state || !walk_begun(p))
-        gated_states_body<D>(m, p, n_items, false, smem, tmem, blockIdx.x, n_state);
+        gated_states_body<D, false>(m, p, n_items, false, smem, tmem, blockIdx.x, n_state);
     gated_out_body<D>(m, p, smem, tmem);
     give_tmem(tmem);
 }
@@ -1698,13 +1699,13 @@ cudaError_t raise_smem(PerDeviceOnce& once, F kern, int bytes) {
 }
 unsigned grid_for(int64_t items, int num_sms) { return static_cast<unsigned>(items < num_sms ? items : num_sms); }
 
-template <int D>
+template <int D, bool ALONE>
 cudaError_t states_d(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
-    cudaError_t e = raise_smem(once, gated_states_tc_kernel<D>, StCfg<D>::SMEM);
+    cudaError_t e = raise_smem(once, gated_states_tc_kernel<D, ALONE>, StCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t items = p.n_units * p.segs * (grad ? 2 : 1);
-    gated_states_tc_kernel<D><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items, grad);
+    gated_states_tc_kernel<D, ALONE><<<grid_for(items, num_sms), StCfg<D>::kThreads, StCfg<D>::SMEM, s>>>(m, p, items, grad);
     return cudaGetLastError();
 }
 template <int D>
@@ -1737,7 +1738,9 @@ cudaError_t grad_d(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaS
 }  // namespace
 
 cudaError_t launch_gated_states_tc(const GatedProblem& p, const GatedMaps& m, bool grad, int num_sms, cudaStream_t s) {
-    return p.dk == 128 ? states_d<128>(p, m, grad, num_sms, s) : states_d<64>(p, m, grad, num_sms, s);
+    const bool alone = grad && !p.sums && (p.cu != nullptr || p.rows <= C);
+    if (p.dk == 128) return alone ? states_d<128, true>(p, m, grad, num_sms, s) : states_d<128, false>(p, m, grad, num_sms, s);
+    return alone ? states_d<64, true>(p, m, grad, num_sms, s) : states_d<64, false>(p, m, grad, num_sms, s);
 }
 cudaError_t launch_gated_prefill_tc(const GatedProblem& p, const GatedMaps& m, int num_sms, cudaStream_t s) {
     return p.dk == 128 ? prefill_d<128>(p, m, num_sms, s) : prefill_d<64>(p, m, num_sms, s);
