@@ -158,8 +158,8 @@ la_status la_decode_step(const void* q, const void* k, const void* v, void* o,
  * starts afresh).  g is [B, H, T] ([1, H, T_total] packed, [B, H] for one
  * token) in `dtype`; NULL means no decay, the recurrence of la_prefill (which
  * computes it in half the time and without a workspace).
- * Gates below -110 count as -110, which decays to zero.  Positive gates are taken as they
- * are while the sum of those of any 128 tokens stays below 80.
+ * Gates below -110 count as -110, which decays to zero.  Positive gates are
+ * taken as they are while the sum of those of any 128 tokens stays below 80.
  * A stretch of gates that decays below 2^-126 may count as zero, whatever
  * positive gates follow it.
  * Inputs are finite apart from gates of -inf: a NaN or infinity in q, k, v or
@@ -203,7 +203,7 @@ size_t la_gated_prefill_workspace_size(la_dtype dtype, int B, int H, int64_t T,
 
 /* Which kernel la_gated_prefill runs: max_tokens is T for dense input and
  * max_seqlen for packed input.  "short", "tc", "simt" or "unsupported".  Host
- * only.  (Of the gradient's: see there.) */
+ * only.  (The gradient's choice stands there.) */
 const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens,
                                     int d_k, int d_v);
 
@@ -219,10 +219,11 @@ const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens,
  *     gate lets little through, dg is off by fp32 of the size of those terms
  *     (q . dq, k . dk), not of its own.
  *   workspace: la_gated_prefill_backward_workspace_size() bytes, as above.
- * Kernels: those of la_gated_prefill, but "short", and "simt" for at most 32
- * tokens of at most 32 units (dense) of any size.
+ * Kernels: "tc" and "simt", as for la_gated_prefill, but "simt" also for dense
+ * calls of at most 32 tokens and 32 units.
  * Nothing is taken from the forward call but its inputs: the states are made
- * again.  dq holds intermediate values until the call's work has finished.  Results do not depend on any order of execution.  Errors as for
+ * again.  dq holds intermediate values until the call's work has finished.
+ * Results do not depend on any order of execution.  Errors as for
  * la_gated_prefill. */
 la_status la_gated_prefill_backward(const void* q, const void* k,
                                     const void* v, const void* g,

@@ -20,9 +20,9 @@
 // T8192: 420 to 450 us in a long run; the floor of its bytes is 167, and the
 // ungated prefill, which walks a unit and makes its outputs in one CTA and reads
 // every byte once, takes 215.  (Times that compare two forms below were taken in
-// turn in short runs, where this case takes 370.)  The gradient moves 955 MB at B4 H16 T4096 where 483 are the least: both
-// states at 72 % of the copy rate (145 us of B4 H16 T8192), then the chunks at
-// 58 %, each a chain of seven products and the steps between them that takes a CTA
+// turn in short runs, where this case takes 370.)  The gradient moves 955 MB at
+// B4 H16 T4096 where 483 are the least: both states at 72 % of the copy rate
+// (145 us of B4 H16 T8192), then the chunks at 58 %, each a chain of seven products and the steps between them that takes a CTA
 // 16k clocks (272 us); in all 455 to 485 us, floor 145.
 //
 // Rounding.  Sums, states and decays are fp32.  An operand of a product is
