@@ -219,8 +219,8 @@ const char* la_gated_prefill_kernel(la_dtype dtype, int64_t max_tokens,
  *     gate lets little through, dg is off by fp32 of the size of those terms
  *     (q . dq, k . dk), not of its own.
  *   workspace: la_gated_prefill_backward_workspace_size() bytes, as above.
- * Kernels: "tc" and "simt", as for la_gated_prefill, but "simt" also for dense
- * calls of at most 32 tokens and 32 units.
+ * Kernels: "tc" and "simt", as for la_gated_prefill, but "simt" also for calls
+ * of at most 32 tokens (packed: in all) and 32 units.
  * Nothing is taken from the forward call but its inputs: the states are made
  * again.  dq holds intermediate values until the call's work has finished.
  * Results do not depend on any order of execution.  Errors as for

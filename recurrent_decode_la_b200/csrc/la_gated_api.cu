@@ -30,15 +30,15 @@ Kernel choose(la_dtype dtype, int64_t max_tokens, int dk, int dv, bool grad) {
     return kSimt;
 }
 
-// The gradient of few short dense units runs on the CUDA cores where the tensor cores could take it: one chunk of 32 tokens
-// in fp32 throughout.  A gate's gradient is a sum of large terms that may cancel, and the bf16 operands that it is made of
+// The gradient of few short units (T: all rows of packed ones) runs on the CUDA cores where the tensor cores could take it:
+// one chunk of 32 tokens each, in fp32 throughout.  A gate's gradient is a sum of large terms that may cancel, and the bf16 operands that it is made of
 // on the tensor cores show in it where few others stand beside it: dg of a single unit of 5 tokens at d 128 was over 0.005
 // of itself off in 4 of 100 calls and up to 0.016 (here 0.0036 at most); of 32 units never.  20 tokens: 6 units at d 64 21
 // us, on the tensor cores 25, 64 units 25 and 26; at d 128 38 and 33, 51 and 37 (512 units: 309 and 136).
 constexpr int64_t kFewUnits = 32, kFewTokens = kGatedSimtChunk;
-Kernel choose_grad(la_dtype dtype, int64_t units, int64_t T, int dk, int dv, bool packed) {
+Kernel choose_grad(la_dtype dtype, int64_t units, int64_t T, int dk, int dv) {
     const Kernel kind = choose(dtype, 0, dk, dv, true);
-    return kind == kTc && !packed && units <= kFewUnits && T <= kFewTokens ? kSimt : kind;
+    return kind == kTc && units <= kFewUnits && T <= kFewTokens ? kSimt : kind;
 }
 
 // CTAs that the split of few units aims at: one a SM of the part this is written for.  Not the current device's count: the
@@ -91,11 +91,15 @@ size_t workspace_bytes_for(la_dtype dtype, int B, int H, int64_t T, int dk, int 
     if ((dtype != LA_F32 && dtype != LA_BF16) || B <= 0 || H <= 0 || T <= 0 || num_seqs < 0) return 0;
     const int64_t groups = static_cast<int64_t>(num_seqs > 0 ? 1 : B) * H;
     if (grad) {
-        const size_t bytes = plan(choose_grad(dtype, groups, T, dk, dv, num_seqs > 0), groups, T, dk, dv, num_seqs, true).bytes;
-        if (num_seqs > 0) return bytes;
+        auto need = [&](int64_t groups, int64_t T, int n) {
+            return plan(choose_grad(dtype, groups * std::max(1, n), T, dk, dv), groups, T, dk, dv, n, true).bytes;
+        };
+        size_t bytes = need(groups, T, num_seqs);
         // room for any call with fewer units or tokens too
-        const int64_t few = std::min(groups, kFewUnits), t = std::min(T, kFewTokens);
-        return std::max(bytes, plan(choose_grad(dtype, few, t, dk, dv, false), few, t, dk, dv, 0, true).bytes);
+        for (int64_t few = 1; few <= std::min(groups, kFewUnits); ++few)
+            bytes = std::max(bytes, need(few, std::min(T, kFewTokens),
+                                         static_cast<int>(std::min<int64_t>(num_seqs, kFewUnits / few))));
+        return bytes;
     }
     // packed input, whose longest sequence is not known here, may need the chunked kernels
     const Kernel kind = choose(dtype, num_seqs > 0 ? 0 : T, dk, dv, false);
@@ -266,7 +270,7 @@ la_status la_gated_prefill_backward(const void* q, const void* k, const void* v,
     if (st != LA_OK || p.n_units == 0) return st;
     if (!q || !k || !v || !d_o || !dstate || !dq || !dk || !dv)
         return refuse(LA_ERR_INVALID_ARG, "a tensor is NULL");
-    const Kernel kind = choose_grad(dtype, p.groups, T, d_k, d_v, p.cu != nullptr);
+    const Kernel kind = choose_grad(dtype, p.n_units, T, d_k, d_v);
     const Layout w = plan(kind, p.groups, T, d_k, d_v, p.num_seqs, true);
     if ((st = place(p, w, workspace, workspace_bytes)) != LA_OK) return st;
     p.q = q; p.k = k; p.v = v; p.g = g;

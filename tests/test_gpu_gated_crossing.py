@@ -55,6 +55,18 @@ def test_states_of_random_signs(dtype, d, T, lens):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,H", [([1], 1), ([0, 5], 1), ([3, 0, 2], 1), ([20, 12], 16), ([1, 1], 17), ([20, 13], 16)])
+def test_short_packed_units(d, lens, H):
+    err = norm = 0.0
+    for seed in range(8):
+        x = make(400 + seed, BF16, 1, H, sum(lens), d, d, "mild", lens)
+        want = ref.prefill_backward(x["q"], x["k"], x["v"], x["g"], x["S0"], x["do"], x["dS"], lens)[3]
+        err += np.linalg.norm(ref.f64(run_backward(x)[3]) - want) ** 2
+        norm += np.linalg.norm(want) ** 2
+    assert err <= 2.0 ** -16 * norm, (err / norm) ** 0.5
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("T,H", [(1, 1), (1, 2), (1, 33), (5, 1), (5, 33), (20, 1), (20, 33), (32, 3), (33, 3)])
 def test_short_units(d, T, H):
     """As they come, eight times over.  A rounding is off by at most 2^-8, evenly spread, so by 2^-8 / sqrt(3) in the mean square:
